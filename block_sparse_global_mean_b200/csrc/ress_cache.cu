@@ -1,0 +1,376 @@
+// Paged 8-bit key/value cache: block tables and slot maps (plan) and the
+// writer (append).
+#include "ress_common.cuh"
+#include "ress_internal.h"
+#include "ress_seq.cuh"
+
+namespace ress {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Plan.  Two exclusive sums over the requests (pages needed, tokens added),
+// then independent lookups: every CTA takes the sums of all requests into its
+// own shared memory and does its share of the table entries and slots, so one
+// launch is enough and no CTA waits for another.
+//
+// Bound by latency: a decoding step moves a few hundred bytes, and even 512
+// requests that add whole views (360,000 slots, 1.4 MB) are a microsecond of
+// bandwidth next to the two dependent loads, the scan and the search.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 512;
+
+struct PlanParams {
+  DeviceError* err;
+  const int32_t* added;
+  const int32_t* lengths;
+  int32_t* table;
+  const int32_t* free_pages;
+  const int32_t* cursor;
+  int32_t* offsets;
+  int32_t* slots;
+  int32_t* new_lengths;
+  int32_t* new_cursor;
+  int requests, max_pages, page, page_log2, pages, n_free, tokens;
+};
+
+// Tokens and new pages of one request.  A request whose numbers are wrong or
+// whose row is too short adds no tokens to the cache and takes no pages (its
+// tokens still stand in the packed order when the count itself is valid).
+struct Ask {
+  int len, add, old_pages, need;
+  bool row_ok;
+};
+__device__ __forceinline__ Ask plan_ask(const PlanParams& p, int r) {
+  Ask a;
+  a.len = p.lengths[r];
+  a.add = p.added[r];
+  const bool numbers = a.len >= 0 && a.add >= 0;
+  a.add = max(a.add, 0);
+  const long long total = (long long)a.len + a.add;
+  const int mask = p.page - 1;
+  a.row_ok = numbers && total <= ((long long)p.max_pages << p.page_log2);
+  a.old_pages = a.row_ok ? (a.len + mask) >> p.page_log2 : 0;
+  a.need = a.row_ok ? (int)((total + mask) >> p.page_log2) - a.old_pages : 0;
+  return a;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanParams p) {
+  extern __shared__ int32_t plan_smem[];
+  int32_t* s_off = plan_smem;                       // [requests + 1] first packed token
+  int32_t* s_first = s_off + p.requests + 1;        // [requests + 1] first new page (of all)
+  int32_t* s_state = s_first + p.requests + 1;      // [requests] length, or -1 when it fails
+  __shared__ longlong2 s_warp[kPlanThreads / 32];
+  __shared__ int s_taken;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool lead = blockIdx.x == 0;
+  const int cursor = p.cursor[0];
+  const bool cursor_ok = cursor >= 0 && cursor <= p.n_free;
+  if (threadIdx.x == 0) s_taken = 0;
+
+  // Both sums run in 64 bits: no counts that int32 arrays can hold overflow them.
+  long long page_sum = 0, token_sum = 0;
+  for (int r0 = 0; r0 < p.requests; r0 += kPlanThreads) {
+    const int r = r0 + threadIdx.x;
+    Ask a{0, 0, 0, 0, false};
+    if (r < p.requests) a = plan_ask(p, r);
+    long long pages = a.need, toks = a.add;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, pages, o);
+      const long long z = __shfl_up_sync(0xffffffffu, toks, o);
+      if (lane >= o) pages += y, toks += z;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = make_longlong2(pages, toks);
+    __syncthreads();
+    long long first = page_sum + pages - a.need, tok = token_sum + toks - a.add;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      const longlong2 sum = s_warp[w];
+      if (w < warp) first += sum.x, tok += sum.y;
+      page_sum += sum.x, token_sum += sum.y;
+    }
+    if (r < p.requests) {
+      const bool tok_ok = tok + a.add <= p.tokens;
+      const bool list_ok = a.need == 0 || (cursor_ok && cursor + first + a.need <= p.n_free);
+      const bool ok = a.row_ok && tok_ok && list_ok;
+      if (lead && !ok)
+        raise_device_error(p.err, RESS_ERR_BAD_INDEX, !a.row_ok ? 100 : !tok_ok ? 102 : 101);
+      s_off[r] = (int)min(tok, 0x7fffffffll);
+      s_first[r] = (int)min(first, 0x7fffffffll);
+      s_state[r] = ok ? a.len : -1;
+      if (ok && lead && a.need > 0) atomicMax(&s_taken, (int)first + a.need);
+    }
+  }
+  if (threadIdx.x == 0) {
+    s_off[p.requests] = (int)min(token_sum, 0x7fffffffll);
+    s_first[p.requests] = (int)min(page_sum, 0x7fffffffll);
+  }
+  __syncthreads();
+
+  // Request r of a flat position: the last one whose first entry is <= i.
+  auto owner = [&](const int32_t* first, int i) {
+    int lo = 0, hi = p.requests - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+  const int stride = gridDim.x * kPlanThreads;
+  const int at = blockIdx.x * kPlanThreads + threadIdx.x;
+  const int mask = p.page - 1;
+
+  for (int r = at; r <= p.requests; r += stride) {
+    p.offsets[r] = s_off[r];
+    if (r < p.requests) {
+      const int len = p.lengths[r];
+      p.new_lengths[r] = s_state[r] >= 0 ? len + p.added[r] : len;
+    }
+  }
+  if (at == 0) p.new_cursor[0] = cursor + s_taken;
+
+  // New table entries.  Positions run over the pages asked for; those of a
+  // request that failed are passed over.
+  const int new_pages = min(s_first[p.requests], p.n_free);
+  for (int i = at; i < new_pages; i += stride) {
+    const int r = owner(s_first, i);
+    if (s_state[r] < 0) continue;
+    const int old_pages = (s_state[r] + mask) >> p.page_log2;
+    const int32_t id = p.free_pages[cursor + i];
+    if (id < 0 || id >= p.pages) raise_device_error(p.err, RESS_ERR_BAD_INDEX, 103);
+    p.table[(size_t)r * p.max_pages + old_pages + (i - s_first[r])] = id;
+  }
+
+  // Slots.  The page of a token is an old table entry or the free-list entry
+  // that the table gets, so nothing written above is read here.
+  for (int t = at; t < p.tokens; t += stride) {
+    int slot = -1;
+    if (t < s_off[p.requests]) {
+      const int r = owner(s_off, t);
+      if (s_state[r] >= 0) {
+        const int pos = s_state[r] + (t - s_off[r]);
+        const int j = pos >> p.page_log2;
+        const int old_pages = (s_state[r] + mask) >> p.page_log2;
+        const int32_t id = j < old_pages ? p.table[(size_t)r * p.max_pages + j]
+                                         : p.free_pages[cursor + s_first[r] + (j - old_pages)];
+        if (id >= 0 && id < p.pages) slot = id * p.page + (pos & mask);
+        else raise_device_error(p.err, RESS_ERR_BAD_INDEX, 103);
+      }
+    }
+    p.slots[t] = slot;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Append.
+// ---------------------------------------------------------------------------
+struct AppendParams {
+  DeviceError* err;
+  const void* x[2];            // new keys, values
+  long long stride[2];         // elements between their token rows
+  const int32_t* slots;
+  uint8_t* cache[2];           // [pages][kv_heads][page][64] codes
+  float* scale[2];             // [pages][kv_heads]
+  int tokens, kv_heads, page, page_log2, pages;
+};
+
+// Exponent e of the smallest power of two with amax <= 448 * 2^e, at least
+// -100: 448 = 1.75 * 2^8, so the mantissa of amax decides between two values.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, -100);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// Two float32 values as e4m3 codes (nearest, ties to even, saturating); a is the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+
+// Eight consecutive values of a token row.
+template <typename T>
+__device__ __forceinline__ void load8(const T* src, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* src, float (&v)[8]) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* src, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(src));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// One warp per (window of tokens, head, tensor): it finds the runs that start
+// in its window (a run: consecutive slots within one page) and for each takes
+// the largest magnitude, the page's scale, then writes the codes.
+template <typename T, int kWindow>
+__global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int which = (int)(w & 1);
+  const int head = (int)((w >> 1) % p.kv_heads);
+  const long long t0 = (w >> 1) / p.kv_heads * kWindow;
+  if (t0 >= p.tokens) return;
+  const int mask = p.page - 1;
+  const int t = (int)t0 + lane;
+  bool starts = false;
+  if (lane < kWindow && t < p.tokens) {
+    const int s = p.slots[t];
+    if (s >= 0) {
+      const int prev = t > 0 ? p.slots[t - 1] : -1;
+      starts = (s & mask) == 0 || prev < 0 || prev + 1 != s;
+    }
+  }
+  unsigned todo = __ballot_sync(0xffffffffu, starts);
+  const T* x = static_cast<const T*>(p.x[which]) + (size_t)head * 64;
+  const long long stride = p.stride[which];
+  const int sub = lane >> 3, col = (lane & 7) * 8;   // four rows of eight 8-value pieces
+  while (todo) {
+    const int first = (int)t0 + __ffs((int)todo) - 1;
+    todo &= todo - 1u;
+    const int slot = p.slots[first];
+    const int page = slot >> p.page_log2, c = slot & mask;
+    if (page >= p.pages) {
+      if (lane == 0) raise_device_error(p.err, RESS_ERR_BAD_INDEX, 104);
+      continue;
+    }
+    // Tokens of the run: those whose slots go on counting, up to the page's end.
+    const int most = min(p.page - c, p.tokens - first);
+    int n = 0;
+    for (int i0 = 0; i0 < most; i0 += 32) {
+      const int i = i0 + lane;
+      const unsigned on = __ballot_sync(0xffffffffu, i < most && p.slots[first + i] == slot + i);
+      if (on != 0xffffffffu) {
+        n = i0 + __ffs((int)~on) - 1;
+        break;
+      }
+      n = i0 + 32;
+    }
+    float amax = 0.f;
+    for (int i = sub; i < n; i += 4) {
+      float v[8];
+      load8(x + (first + i) * stride + col, v);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(v[u]));
+    }
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    float* scale_at = p.scale[which] + (size_t)page * p.kv_heads + head;
+    const float old = c > 0 ? *scale_at : 0.f;
+    const float now = fmaxf(pow2(scale_exponent(amax)), old);
+    const float inv = 1.0f / now;   // exact: a power of two
+    uint8_t* dst = p.cache[which] + (((size_t)page * p.kv_heads + head) << p.page_log2) * 64;
+    for (int i = sub; i < n; i += 4) {
+      float v[8];
+      load8(x + (first + i) * stride + col, v);
+      uint2 o;
+      o.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
+      o.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
+      *reinterpret_cast<uint2*>(dst + (size_t)(c + i) * 64 + col) = o;
+    }
+    if (now != old) {
+      __syncwarp();
+      if (lane == 0) *scale_at = now;
+      const float ratio = old * inv;
+      for (int i = lane; i < c * 16; i += 32) {   // older codes, four at a time
+        uint32_t* at = reinterpret_cast<uint32_t*>(dst) + i;
+        const uint32_t codes = *at;
+        const float2 a = from_e4m3x2(codes & 0xffffu), b = from_e4m3x2(codes >> 16);
+        *at = e4m3x2(a.x * ratio, a.y * ratio) | e4m3x2(b.x * ratio, b.y * ratio) << 16;
+      }
+    }
+  }
+}
+
+template <typename T>
+void launch_append_typed(const AppendParams& p, cudaStream_t st) {
+  // Short calls (a few tokens each in a page of its own) take a warp per
+  // token, long ones (whole pages) a warp per 32 tokens.
+  const int window = p.tokens <= 1024 ? 1 : 32;
+  const long long warps = ((long long)p.tokens + window - 1) / window * p.kv_heads * 2;
+  const unsigned blocks = (unsigned)((warps + 7) / 8);
+  if (window == 1) cache_append_kernel<T, 1><<<blocks, 256, 0, st>>>(p);
+  else cache_append_kernel<T, 32><<<blocks, 256, 0, st>>>(p);
+}
+
+}  // namespace
+
+ress_status launch_cache_plan(const ress_cache_shape& s, const int32_t* added,
+                              const int32_t* lengths, int32_t* table, const int32_t* free_pages,
+                              int32_t n_free, const int32_t* cursor, int32_t tokens,
+                              int32_t* offsets, int32_t* slots, int32_t* new_lengths,
+                              int32_t* new_cursor, cudaStream_t st) {
+  PlanParams p{};
+  p.err = device_error_ptr();
+  if (p.err == nullptr) return RESS_ERR_CUDA;
+  p.added = added;
+  p.lengths = lengths;
+  p.table = table;
+  p.free_pages = free_pages;
+  p.cursor = cursor;
+  p.offsets = offsets;
+  p.slots = slots;
+  p.new_lengths = new_lengths;
+  p.new_cursor = new_cursor;
+  p.requests = s.requests;
+  p.max_pages = s.max_pages;
+  p.page = s.page;
+  p.page_log2 = s.page == 64 ? 6 : 7;
+  p.pages = s.pages;
+  p.n_free = n_free;
+  p.tokens = tokens;
+  const size_t smem = sizeof(int32_t) * (3 * (size_t)s.requests + 2);
+  if (smem > 48 * 1024)
+    if (ress_status e = record_cuda(cudaFuncSetAttribute(
+            cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+      return e;
+  const long long items = (long long)tokens + s.requests;
+  const long long blocks = (items + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
+  cache_plan_kernel<<<(unsigned)(blocks < 1 ? 1 : blocks > 148 ? 148 : blocks), kPlanThreads, smem,
+                      st>>>(p);
+  return record_cuda(cudaGetLastError());
+}
+
+ress_status launch_cache_append(const ress_cache_shape& s, const void* k, const void* v, bool f32,
+                                int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                                int32_t tokens, void* k_cache, void* v_cache, float* k_scale,
+                                float* v_scale, cudaStream_t st) {
+  AppendParams p{};
+  p.err = device_error_ptr();
+  if (p.err == nullptr) return RESS_ERR_CUDA;
+  p.x[0] = k;
+  p.x[1] = v;
+  p.stride[0] = k_stride;
+  p.stride[1] = v_stride;
+  p.slots = slots;
+  p.cache[0] = static_cast<uint8_t*>(k_cache);
+  p.cache[1] = static_cast<uint8_t*>(v_cache);
+  p.scale[0] = k_scale;
+  p.scale[1] = v_scale;
+  p.tokens = tokens;
+  p.kv_heads = s.kv_heads;
+  p.page = s.page;
+  p.page_log2 = s.page == 64 ? 6 : 7;
+  p.pages = s.pages;
+  if (f32) launch_append_typed<float>(p, st);
+  else launch_append_typed<__nv_bfloat16>(p, st);
+  return record_cuda(cudaGetLastError());
+}
+
+}  // namespace ress

@@ -9,8 +9,9 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -46,7 +47,24 @@ class ress_layout(ctypes.Structure):
                 ("special_tokens", ctypes.c_int32)]
 
 
+class ress_cross_shape(ctypes.Structure):
+    _fields_ = [("nq", ctypes.c_int64), ("nk", ctypes.c_int64), ("seqs", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class ress_cache_shape(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("requests", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
+_I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
+_SIZE = ctypes.c_size_t
 _SHAPE = ctypes.POINTER(ress_shape)
 
 lib.ress_version.restype = ctypes.c_int
@@ -99,6 +117,25 @@ lib.ress_select_blocks_vasc.argtypes = [_SHAPE, _P, _P, _P, _P, ctypes.c_int32, 
                                         ctypes.c_int32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
 lib.ress_validate_idx.restype = ctypes.c_int
 lib.ress_validate_idx.argtypes = [_SHAPE, ctypes.c_int32, _P, _P]
+_CROSS = ctypes.POINTER(ress_cross_shape)
+lib.ress_cross_workspace_bytes.restype = _SIZE
+lib.ress_cross_workspace_bytes.argtypes = [_CROSS]
+lib.ress_cross_bwd_workspace_bytes.restype = _SIZE
+lib.ress_cross_bwd_workspace_bytes.argtypes = [_CROSS]
+lib.ress_cross_attn.restype = ctypes.c_int
+lib.ress_cross_attn.argtypes = [_CROSS] + [_P] * 10 + [_SIZE, _P]
+lib.ress_cross_attn_bwd.restype = ctypes.c_int
+lib.ress_cross_attn_bwd.argtypes = [_CROSS] + [_P] * 14 + [_SIZE, _P]
+_CACHE = ctypes.POINTER(ress_cache_shape)
+lib.ress_cache_plan.restype = ctypes.c_int
+lib.ress_cache_plan.argtypes = [_CACHE, _P, _P, _P, _P, _I32, _P, _I32, _P, _P, _P, _P, _P]
+lib.ress_cache_append.restype = ctypes.c_int
+lib.ress_cache_append.argtypes = [_CACHE, _P, _P, _I32, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P]
+lib.ress_cache_attn_workspace_bytes.restype = _SIZE
+lib.ress_cache_attn_workspace_bytes.argtypes = [_CACHE, _I32, _I32]
+lib.ress_cache_attn.restype = ctypes.c_int
+lib.ress_cache_attn.argtypes = ([_CACHE, _I32, _I32, _P, _I64] + [_P] * 7 + [_I32] + [_P] * 3
+                                + [_SIZE, _P])
 lib.ress_check_device_errors.restype = ctypes.c_int
 lib.ress_check_device_errors.argtypes = [_P, ctypes.POINTER(ctypes.c_int32)]
 
@@ -563,6 +600,322 @@ def ress_validate_idx(idx: torch.Tensor, n: int, block: int,
     status = _on(idx.device, lib.ress_validate_idx, ctypes.byref(sh), int(idx.shape[2]), _ptr(idx),
                  _stream_ptr(stream, idx.device))
     _check(status, "ress_validate_idx")
+
+
+# --------------------------------------------------------------------------------------------
+# Keys of another length, and the 8-bit cache
+# --------------------------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _cross_shape(nq: int, nk: int, seqs: int, heads: int, kv_heads: int, head_dim: int,
+                 q_stride: int, k_stride: int, v_stride: int):
+    sh = ctypes.byref(ress_cross_shape(nq, nk, seqs, heads, kv_heads, head_dim, RESS_BF16,
+                                       q_stride, k_stride, v_stride))
+    return (sh, int(lib.ress_cross_workspace_bytes(sh)),
+            int(lib.ress_cross_bwd_workspace_bytes(sh)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_shape(pages: int, page: int, kv_heads: int, head_dim: int, requests: int,
+                 max_pages: int):
+    return ctypes.byref(ress_cache_shape(pages, page, kv_heads, head_dim, requests, max_pages))
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_attn_bytes(pages: int, page: int, kv_heads: int, head_dim: int, requests: int,
+                      max_pages: int, heads: int, tokens: int) -> int:
+    sh = _cache_shape(pages, page, kv_heads, head_dim, requests, max_pages)
+    return int(lib.ress_cache_attn_workspace_bytes(sh, heads, tokens))
+
+
+def _run_on(device: torch.device, stream: Optional[torch.cuda.Stream], fn, *args) -> int:
+    """``_on`` with the stream as the last argument, without a device switch
+    where ``device`` is current already."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream_ptr(stream, device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_ptr(stream, device))
+
+
+def _new(shape, dtype: torch.dtype, device: torch.device,
+         stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new tensor for a call on ``stream``: allocated on that stream, so that
+    the caching allocator hands its memory to no one before the call is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, device: torch.device,
+             stream: Optional[torch.cuda.Stream]) -> Tuple[Optional[int], int, object]:
+    """(pointer, bytes, owner) of a call's workspace."""
+    if workspace is not None:
+        _check_workspace(workspace, device)
+        return _ptr(workspace), workspace.numel(), workspace
+    if need == 0:
+        return None, 0, None
+    ws = _new((need,), torch.uint8, device, stream)
+    return ws.data_ptr(), need, ws
+
+
+def _token_rows(t: torch.Tensor, name: str) -> int:
+    """Elements between the token rows of [n, heads, d] (0: dense).  Rows may
+    be slices of wider ones; the values of a row stand together."""
+    if t.is_contiguous():
+        return 0
+    s0, s1, s2 = t.stride()
+    _, h, d = t.shape
+    if s2 != 1 or (h > 1 and s1 != d) or s0 < h * d:
+        raise ValueError(f"{name}: the heads of a token must stand together")
+    return s0
+
+
+def _check_rows(t: torch.Tensor, name: str, device: torch.device, heads: Optional[int] = None,
+                dtypes=(torch.bfloat16,)) -> None:
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d]")
+    if heads is not None and t.shape[1] != heads:
+        raise ValueError(f"{name} has {t.shape[1]} heads, expected {heads}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+
+
+def _seq_arrays(q_offsets, kv_offsets, q_lens, kv_lens, device: torch.device) -> int:
+    """Checks the arrays of a packed batch; returns the number of sequences."""
+    if (q_offsets is None) != (kv_offsets is None):
+        raise ValueError("q_offsets and kv_offsets come together")
+    seqs = 1
+    if q_offsets is not None:
+        if q_offsets.dim() != 1 or q_offsets.shape[0] < 2:
+            raise ValueError("q_offsets must be [sequences + 1]")
+        seqs = q_offsets.shape[0] - 1
+        _check_buffer(q_offsets, (seqs + 1,), torch.int32, device, "q_offsets")
+        _check_buffer(kv_offsets, (seqs + 1,), torch.int32, device, "kv_offsets")
+    for name, t in (("q_lens", q_lens), ("kv_lens", kv_lens)):
+        if t is not None:
+            _check_buffer(t, (seqs,), torch.int32, device, name)
+    return seqs
+
+
+def _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens):
+    device = q.device
+    _check_rows(q, "q", device)
+    _check_rows(k, "k", device)
+    if tuple(v.shape) != tuple(k.shape):
+        raise ValueError(f"v has shape {tuple(v.shape)}, k has {tuple(k.shape)}")
+    _check_rows(v, "v", device)
+    if k.shape[2] != q.shape[2]:
+        raise ValueError(f"k has head dim {k.shape[2]}, q has {q.shape[2]}")
+    seqs = _seq_arrays(q_offsets, kv_offsets, q_lens, kv_lens, device)
+    return _cross_shape(q.shape[0], k.shape[0], seqs, q.shape[1], k.shape[1], q.shape[2],
+                        _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v"))
+
+
+def ress_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    q_offsets: Optional[torch.Tensor] = None,
+                    kv_offsets: Optional[torch.Tensor] = None,
+                    q_lens: Optional[torch.Tensor] = None, kv_lens: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    want_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None
+                    ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of q [nq, H, 64] over k, v [nk, Hk, 64] (bf16, Hk divides H):
+    returns (out [nq, H, 64], lse [H, nq] float32 or None).
+
+    ``q_offsets`` / ``kv_offsets`` ([sequences + 1] int32) pack several
+    sequences; ``q_lens`` / ``kv_lens`` ([sequences] int32) mark the rows of
+    each that are not padding.  Token rows of q, k and v may be slices of
+    wider rows.  Rows of no sequence are left as they were (undefined in a
+    tensor that this call allocates).  See include/ress.h."""
+    sh, need, _ = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
+    device, (nq, h, _) = q.device, q.shape
+    if out is None:
+        out = _new(q.shape, q.dtype, device, stream)
+    else:
+        _check_buffer(out, q.shape, q.dtype, device, "out")
+    if lse is not None:
+        _check_buffer(lse, (h, nq), torch.float32, device, "lse")
+    elif want_lse:
+        lse = _new((h, nq), torch.float32, device, stream)
+    ws, size, owner = _scratch(workspace, need, device, stream)
+    status = _run_on(device, stream, lib.ress_cross_attn, sh, q.data_ptr(), k.data_ptr(),
+                     v.data_ptr(), _ptr(q_offsets), _ptr(kv_offsets), _ptr(q_lens), _ptr(kv_lens),
+                     _ptr(out), _ptr(lse), ws, size)
+    _check(status, "ress_cross_attn")
+    return out, lse
+
+
+def ress_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                        lse: torch.Tensor, dout: torch.Tensor,
+                        q_offsets: Optional[torch.Tensor] = None,
+                        kv_offsets: Optional[torch.Tensor] = None,
+                        q_lens: Optional[torch.Tensor] = None,
+                        kv_lens: Optional[torch.Tensor] = None,
+                        dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                        dv: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None
+                        ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of ress_cross_attn: returns (dq, dk, dv) in the shapes of q,
+    k and v, from what the forward call returned and dout [nq, H, 64]."""
+    sh, _, need = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
+    device, (nq, h, _) = q.device, q.shape
+    _check_buffer(out, q.shape, q.dtype, device, "out")
+    _check_buffer(dout, q.shape, q.dtype, device, "dout")
+    _check_buffer(lse, (h, nq), torch.float32, device, "lse")
+    grads = []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
+        if t is None:
+            t = _new(like.shape, like.dtype, device, stream)
+        else:
+            _check_buffer(t, like.shape, like.dtype, device, name)
+        grads.append(t)
+    ws, size, owner = _scratch(workspace, need, device, stream)
+    status = _run_on(device, stream, lib.ress_cross_attn_bwd, sh, q.data_ptr(), k.data_ptr(),
+                     v.data_ptr(), _ptr(out), _ptr(lse), _ptr(dout), _ptr(q_offsets),
+                     _ptr(kv_offsets), _ptr(q_lens), _ptr(kv_lens), _ptr(grads[0]),
+                     _ptr(grads[1]), _ptr(grads[2]), ws, size)
+    _check(status, "ress_cross_attn_bwd")
+    return grads[0], grads[1], grads[2]
+
+
+class ress_cache(NamedTuple):
+    """A paged 8-bit cache: codes [pages, Hk, page, 64] float8_e4m3fn and
+    scales [pages, Hk] float32 of the keys and the values."""
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def make_cache(pages: int, kv_heads: int, page: int, device="cuda") -> ress_cache:
+    """An empty pool of ``pages`` pages of ``page`` (64 or 128) tokens."""
+    codes = [torch.zeros((pages, kv_heads, page, 64), dtype=torch.float8_e4m3fn, device=device)
+             for _ in range(2)]
+    return ress_cache(*codes, *(torch.zeros((pages, kv_heads), dtype=torch.float32, device=device)
+                                for _ in range(2)))
+
+
+def _check_cache(cache: ress_cache, device: torch.device) -> Tuple[int, int, int, int]:
+    """(pages, page, kv_heads, head_dim) of a cache whose parts fit together."""
+    if cache.k.dim() != 4:
+        raise ValueError("cache.k must be [pages, heads, page, d]")
+    pages, heads, page, d = cache.k.shape
+    _check_buffer(cache.k, cache.k.shape, torch.float8_e4m3fn, device, "cache.k")
+    _check_buffer(cache.v, cache.k.shape, torch.float8_e4m3fn, device, "cache.v")
+    _check_buffer(cache.k_scale, (pages, heads), torch.float32, device, "cache.k_scale")
+    _check_buffer(cache.v_scale, (pages, heads), torch.float32, device, "cache.v_scale")
+    return pages, page, heads, d
+
+
+def ress_cache_plan(added: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
+                    free_pages: torch.Tensor, cursor: torch.Tensor, page: int, tokens: int,
+                    pages: Optional[int] = None, offsets: Optional[torch.Tensor] = None,
+                    slots: Optional[torch.Tensor] = None,
+                    new_lengths: Optional[torch.Tensor] = None,
+                    new_cursor: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None
+                    ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Block tables and slot maps for ``added`` [R] tokens behind ``lengths``
+    [R] cached ones: extends ``table`` [R, max_pages] in place from
+    ``free_pages[cursor:]`` and returns (offsets [R + 1], slots [tokens],
+    new_lengths [R], new_cursor [1]), all int32.  ``tokens`` is the length of
+    the slot map (at least the sum of ``added``); ``pages`` bounds the page ids
+    (default: the largest pool).  See include/ress.h."""
+    device = added.device
+    if added.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("added must be [R], table [R, max_pages], free_pages [n]")
+    r, width = table.shape
+    for name, t, shape in (("added", added, (r,)), ("lengths", lengths, (r,)),
+                           ("table", table, (r, width)),
+                           ("free_pages", free_pages, free_pages.shape), ("cursor", cursor, (1,))):
+        _check_buffer(t, shape, torch.int32, device, name)
+    made = []
+    for name, t, n in (("offsets", offsets, r + 1), ("slots", slots, int(tokens)),
+                       ("new_lengths", new_lengths, r), ("new_cursor", new_cursor, 1)):
+        if t is None:
+            t = _new((n,), torch.int32, device, stream)
+        else:
+            _check_buffer(t, (n,), torch.int32, device, name)
+        made.append(t)
+    limit = (2 ** 31 - 1) // max(int(page), 1) if pages is None else pages
+    status = _run_on(device, stream, lib.ress_cache_plan,
+                     _cache_shape(limit, int(page), 1, 64, r, width), _ptr(added), _ptr(lengths),
+                     _ptr(table), _ptr(free_pages), free_pages.shape[0], _ptr(cursor),
+                     int(tokens), _ptr(made[0]), _ptr(made[1]), _ptr(made[2]), _ptr(made[3]))
+    _check(status, "ress_cache_plan")
+    return made[0], made[1], made[2], made[3]
+
+
+def ress_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: ress_cache,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Writes the tokens k, v [tokens, Hk, 64] (bf16 or float32; rows may be
+    slices of wider ones) into the cells ``slots`` [tokens] int32 of ``cache``,
+    in place; negative slots skip their token.  See include/ress.h."""
+    device = k.device
+    pages, page, heads, d = _check_cache(cache, device)
+    _check_rows(k, "k", device, heads, (torch.bfloat16, torch.float32))
+    if tuple(v.shape) != tuple(k.shape) or k.shape[2] != d:
+        raise ValueError(f"k and v must be [tokens, {heads}, {d}], got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    _check_rows(v, "v", device, heads, (k.dtype,))
+    _check_buffer(slots, (k.shape[0],), torch.int32, device, "slots")
+    status = _run_on(device, stream, lib.ress_cache_append,
+                     _cache_shape(pages, page, heads, d, 1, 1), k.data_ptr(), v.data_ptr(),
+                     RESS_F32 if k.dtype == torch.float32 else RESS_BF16, _token_rows(k, "k"),
+                     _token_rows(v, "v"), _ptr(slots), k.shape[0], _ptr(cache.k), _ptr(cache.v),
+                     _ptr(cache.k_scale), _ptr(cache.v_scale))
+    _check(status, "ress_cache_append")
+
+
+def ress_cache_attn(q: torch.Tensor, cache: ress_cache, table: torch.Tensor,
+                    lengths: torch.Tensor, offsets: torch.Tensor, step: int = 0,
+                    out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    want_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None
+                    ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of the newest tokens q [T, H, 64] (bf16) of every request over
+    its cached tokens: returns (out [T, H, 64], lse [H, T] float32 or None).
+
+    ``offsets`` [R + 1] packs the query rows of the requests, ``lengths`` [R]
+    counts their cached tokens (the queries' own among them), ``table`` [R,
+    max_pages] names their pages.  ``step`` 0: every query sees all of its
+    request; 1: causal; n: groups of n tokens see themselves and the earlier
+    groups.  See include/ress.h."""
+    device = q.device
+    pages, page, heads, d = _check_cache(cache, device)
+    _check_rows(q, "q", device)
+    if q.shape[2] != d:
+        raise ValueError(f"q has head dim {q.shape[2]}, the cache {d}")
+    if table.dim() != 2:
+        raise ValueError("table must be [requests, max_pages]")
+    r, width = table.shape
+    _check_buffer(table, (r, width), torch.int32, device, "table")
+    _check_buffer(lengths, (r,), torch.int32, device, "lengths")
+    _check_buffer(offsets, (r + 1,), torch.int32, device, "offsets")
+    n, h, _ = q.shape
+    if out is None:
+        out = _new(q.shape, q.dtype, device, stream)
+    else:
+        _check_buffer(out, q.shape, q.dtype, device, "out")
+    if lse is not None:
+        _check_buffer(lse, (h, n), torch.float32, device, "lse")
+    elif want_lse:
+        lse = _new((h, n), torch.float32, device, stream)
+    ws, size, owner = _scratch(workspace, _cache_attn_bytes(pages, page, heads, d, r, width, h, n),
+                               device, stream)
+    status = _run_on(device, stream, lib.ress_cache_attn,
+                     _cache_shape(pages, page, heads, d, r, width), h, n, q.data_ptr(),
+                     _token_rows(q, "q"), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
+                     _ptr(cache.v_scale), _ptr(table), _ptr(lengths), _ptr(offsets), int(step),
+                     _ptr(out), _ptr(lse), ws, size)
+    _check(status, "ress_cache_attn")
+    return out, lse
 
 
 def ress_check_device_errors(stream: Optional[torch.cuda.Stream] = None,

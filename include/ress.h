@@ -14,6 +14,12 @@
  * ress_select_blocks_cdf is the SparseVGGT variant of stage 1: a per-row
  * cumulative probability threshold instead of a fixed budget.
  *
+ * Next to the three stages stand operators for tokens that meet keys of
+ * another length: ress_cross_attn and its gradients ress_cross_attn_bwd
+ * (packed sequences), and, for views that arrive one after another, a paged
+ * key/value cache in 8 bits: ress_cache_plan (block tables and slot maps),
+ * ress_cache_append (the writer) and ress_cache_attn (attention over it).
+ *
  * Sources: ReSS: Residual-Restoring Sparse Attention for 3D Vision Transformers
  * (thelatestinai.com) - Abstract, Fig. 1, Fig. 3, Table 1, Table S5, Table S6;
  * VASC: Value-Aware Sparse Attention with Cross-Layer Memory (paperlayer.ai) -
@@ -428,6 +434,225 @@ ress_status ress_block_drift_layout(const ress_shape* shape, const ress_layout* 
                                     const int32_t* idx, const float* lse, float* drift,
                                     float* set_drift, void* workspace, size_t workspace_bytes,
                                     void* stream);
+
+/*
+ * Shape of ress_cross_attn and ress_cross_attn_bwd: packed sequences of
+ * query tokens and of key tokens, which need not be equally long.
+ *
+ * q, out, dout, dq are [nq][heads][64], k, v, dk, dv are [nk][kv_heads][64];
+ * query head h reads key head h / (heads / kv_heads).  A token row of q, k or
+ * v may be part of a wider row (a slice of a fused projection): q_stride,
+ * k_stride and v_stride are the elements from one token row to the next, a
+ * multiple of 8 and at least the row's own heads * 64; 0 stands for exactly
+ * that.  Every other tensor is dense.
+ *
+ * Sequence b is the query rows q_offsets[b] .. q_offsets[b + 1] - 1 and the
+ * key rows kv_offsets[b] .. kv_offsets[b + 1] - 1 (int32 device arrays of
+ * seqs + 1 entries; both NULL with seqs == 1: all rows).  q_lens and kv_lens
+ * (int32 device arrays of seqs entries, or NULL) mark padding: only the first
+ * q_lens[b] / kv_lens[b] rows of a sequence carry data.  Padding keys enter
+ * no softmax and are never used as numbers (they may hold NaN); a padding
+ * query row writes 0 and lse -inf, and so does a query whose sequence has no
+ * key.  Rows of no sequence (before the first offset, behind the last) are
+ * left as they were in every output.
+ *
+ * The arrays live on the device, so the kernels check them: a sequence whose
+ * offsets are out of range or decrease is taken as empty and flagged
+ * (RESS_ERR_BAD_INDEX, detail 90 for queries, 91 for keys), a length outside
+ * its sequence is clamped to it and flagged (92, 93).
+ *
+ * dtype must be RESS_BF16: the contractions take bf16 operands, and a float32
+ * input would be rounded to them unseen.  1 <= heads <= 64, kv_heads divides
+ * heads, 1 <= seqs <= 8192, nq and nk up to 2^30.
+ */
+typedef struct {
+  int64_t nq;
+  int64_t nk;
+  int32_t seqs;
+  int32_t heads;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+} ress_cross_shape;
+
+/* Workspace bytes of ress_cross_attn / ress_cross_attn_bwd (0: none needed or
+ * the shape is invalid): partial sums where a long key (or query) range is
+ * split over several CTAs, and for the gradients delta [heads][nq] float32. */
+size_t ress_cross_workspace_bytes(const ress_cross_shape* shape);
+size_t ress_cross_bwd_workspace_bytes(const ress_cross_shape* shape);
+
+/*
+ * Attention of one set of tokens over another (dense, bidirectional): for
+ * query row i of sequence b and head h, over the keys t of sequence b,
+ *   out[i][h] = sum_t softmax_t((q[i][h] . k[t][h']) / sqrt(d)) v[t][h'],
+ *   lse[h][i] = ln sum_t exp((q[i][h] . k[t][h']) / sqrt(d)).
+ * Every other entry point of this library attends a sequence to itself; this
+ * one serves queries that are not among the keys (a new view against stored
+ * ones, a decoder's tokens against the encoded views).
+ *
+ *   out        [nq][heads][64] bf16;  lse  [heads][nq] float32, or NULL.
+ *   workspace  ress_cross_workspace_bytes(shape) bytes, 256-byte aligned
+ *              (NULL when that is 0).
+ *   Contractions on bf16 operands with float32 accumulation; probabilities
+ *   enter P V as bf16, their sum and lse are float32 sums of the unrounded
+ *   ones.  Results do not depend on the run: no atomics add numbers.
+ */
+ress_status ress_cross_attn(const ress_cross_shape* shape, const void* q, const void* k,
+                            const void* v, const int32_t* q_offsets, const int32_t* kv_offsets,
+                            const int32_t* q_lens, const int32_t* kv_lens, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of ress_cross_attn.  With P = exp(S - lse), S = q . k / sqrt(d),
+ * delta[i] = dout[i] . out[i] and dS = P (dout . v - delta):
+ *   dq[i] = sum_t dS[i][t] k[t] / sqrt(d),
+ *   dk[t] = sum_i dS[i][t] q[i] / sqrt(d),   dv[t] = sum_i P[i][t] dout[i],
+ * where dk and dv also add over the heads / kv_heads query heads that share a
+ * key head.  Rows without a partner (no key, no query) and padding rows get
+ * 0; rows of no sequence are left as they were.
+ *
+ *   out, lse   as ress_cross_attn wrote them (an lse of -inf marks a row
+ *              without a key).
+ *   dout       [nq][heads][64] bf16.
+ *   dq         [nq][heads][64] bf16; dk, dv [nk][kv_heads][64] bf16.
+ *   workspace  ress_cross_bwd_workspace_bytes(shape) bytes, 256-byte aligned.
+ *   P and dS enter their products as bf16; all sums are float32 in a fixed
+ *   order.
+ */
+ress_status ress_cross_attn_bwd(const ress_cross_shape* shape, const void* q, const void* k,
+                                const void* v, const void* out, const float* lse,
+                                const void* dout, const int32_t* q_offsets,
+                                const int32_t* kv_offsets, const int32_t* q_lens,
+                                const int32_t* kv_lens, void* dq, void* dk, void* dv,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A paged key/value cache in 8 bits for views that arrive one after another.
+ *
+ * The pool holds `pages` pages of `page` tokens (64 or 128, the library's
+ * blocks).  k_cache and v_cache are [pages][kv_heads][page][64] e4m3 codes
+ * (one byte each); k_scale and v_scale are [pages][kv_heads] float32: a page
+ * and head stands for code * scale.  A scale is a power of two: e4m3 has a
+ * binary exponent of its own, so a finer scale would buy no precision, while
+ * a power of two divides and multiplies exactly, and a scale that grows
+ * re-codes older tokens without rounding them again, except where they fall
+ * among e4m3's smallest (subnormal) numbers.  Request r keeps its tokens 0 ..
+ * lengths[r] - 1 in the pages table[r][0], table[r][1], ... ([requests]
+ * [max_pages] int32; entries behind the last page in use are not read).
+ */
+typedef struct {
+  int32_t pages;      /* pages of the pool */
+  int32_t page;       /* tokens per page: 64 or 128; pages * page < 2^31 */
+  int32_t kv_heads;   /* 1..64 */
+  int32_t head_dim;   /* must be 64 */
+  int32_t requests;   /* rows of the table, 1..8192 */
+  int32_t max_pages;  /* entries per table row; max_pages * page < 2^31 */
+} ress_cache_shape;
+
+/*
+ * Block tables and slot maps for the tokens that every request adds.
+ *
+ * Request r holds lengths[r] tokens and adds added[r].  It needs
+ * ceil((lengths[r] + added[r]) / page) - ceil(lengths[r] / page) new pages;
+ * these are taken in request order from free_pages, starting at entry
+ * cursor[0], and written behind the row's pages in use:
+ *   table[r][ceil(lengths[r] / page) + i] = free_pages[cursor + need_0 + ... + need_(r-1) + i].
+ * The added tokens are packed in request order: those of r are offsets[r] ..
+ * offsets[r + 1] - 1, and token t of them goes to cell
+ *   slots[t] = table[r][pos / page] * page + pos % page,  pos = lengths[r] + t - offsets[r].
+ *
+ * A request that does not fit (its row too short, the free list used up
+ * before or in it, more tokens than the slot map holds, a negative length or
+ * count) is left as it is: its length stays, its tokens get slot -1, no page
+ * is taken for it, and the device error RESS_ERR_BAD_INDEX is flagged (detail
+ * 100 row or counts, 101 free list, 102 slot map).  Once the free list or the
+ * slot map is used up, later requests that need of it fail too.  A page id
+ * outside the pool, in the free list or the table, gives its tokens slot -1
+ * and is flagged (103).
+ *
+ *   added, lengths  [requests] int32;  table in/out;  free_pages [n_free] int32.
+ *   cursor          [1] int32: first entry of free_pages not yet taken.
+ *   offsets         out, [requests + 1] int32.
+ *   slots           out, [tokens] int32; entries behind the added tokens get -1.
+ *   new_lengths     out, [requests] int32;  new_cursor  out, [1] int32.
+ *   The outputs other than table must not overlap the inputs (every CTA reads
+ *   the inputs while others write), which the call checks for equal pointers.
+ *   shape->kv_heads and head_dim are not used.  One launch, no workspace.
+ */
+ress_status ress_cache_plan(const ress_cache_shape* shape, const int32_t* added,
+                            const int32_t* lengths, int32_t* table, const int32_t* free_pages,
+                            int32_t n_free, const int32_t* cursor, int32_t tokens,
+                            int32_t* offsets, int32_t* slots, int32_t* new_lengths,
+                            int32_t* new_cursor, void* stream);
+
+/*
+ * Writes new tokens into the cache: token t (row t of k and v, [tokens]
+ * [kv_heads][64] of `dtype`, bf16 or float32, row strides as in
+ * ress_cross_shape) goes to cell slots[t]; a negative slot skips the token.
+ *
+ * Slots of one page must stand together and ascend by one (as
+ * ress_cache_plan writes them): a run.  For each run, head and tensor, with c
+ * the run's first cell and amax the largest |x| of its tokens,
+ *   s = smallest power of two >= 2^-100 with amax <= 448 s,
+ *   s = max(s, old scale) when c > 0;
+ * the page's scale becomes s, the run's codes are x / s rounded to e4m3
+ * (nearest, ties to even), and when c > 0 the codes of cells 0 .. c - 1 are
+ * re-coded to the new scale.  A run that starts at cell 0 takes the page over:
+ * an older scale is forgotten.  Cells behind the run keep their codes.
+ *
+ *   A page that appears in two runs of one call gets an undefined content
+ *   (two runs write it at once); slots outside the pool are skipped and
+ *   flagged (RESS_ERR_BAD_INDEX, detail 104).  Values must be finite: a NaN
+ *   becomes the NaN code, an infinity the largest number of its scale.
+ *   shape->requests and max_pages are not used.  One launch, no workspace.
+ */
+ress_status ress_cache_append(const ress_cache_shape* shape, const void* k, const void* v,
+                              int32_t dtype, int64_t k_stride, int64_t v_stride,
+                              const int32_t* slots, int32_t tokens, void* k_cache,
+                              void* v_cache, float* k_scale, float* v_scale, void* stream);
+
+/*
+ * Workspace bytes of ress_cache_attn (0 if the shape is invalid): partial
+ * rows of requests whose keys are split over several CTAs.
+ */
+size_t ress_cache_attn_workspace_bytes(const ress_cache_shape* shape, int32_t heads,
+                                       int32_t tokens);
+
+/*
+ * Attention of new tokens over the cache.  The queries of request r are the
+ * rows offsets[r] .. offsets[r + 1] - 1 of q ([tokens][heads][64] bf16, row
+ * stride q_stride elements, 0 = dense), the last of the request's lengths[r]
+ * tokens (which have been appended): row i of n stands at position
+ * lengths[r] - n + i.  Query head h reads key head h / (heads / kv_heads).
+ *   out[t][h] = sum_u softmax_u((q . K_u) / sqrt(d)) V_u,  lse[h][t] the log-sum-exp,
+ * over the cached tokens u < end(t):
+ *   step == 0   end = lengths[r]: every token sees every other;
+ *   step >= 1   end = min(lengths[r], (position / step + 1) * step): a token
+ *               sees its own group of `step` tokens and the earlier ones
+ *               (step 1: causal; step = tokens of a view: views in order).
+ * A row that sees nothing (an empty request, a position before 0) writes 0
+ * and lse -inf.  Rows of no request are left as they were.
+ *
+ *   table     [requests][max_pages] int32, lengths [requests] int32, offsets
+ *             [requests + 1] int32.  Flagged as RESS_ERR_BAD_INDEX: offsets
+ *             out of range or descending (detail 90; the request is taken as
+ *             empty), a length outside 0 .. max_pages * page (94; clamped), a
+ *             page outside the pool (95; its keys are left out).
+ *   out       [tokens][heads][64] bf16;  lse [heads][tokens] float32 or NULL.
+ *   workspace ress_cache_attn_workspace_bytes() bytes, 256-byte aligned.
+ *   Codes and queries are multiplied exactly; probabilities enter P V as
+ *   bf16, their sums and lse are float32.  Cells behind lengths[r] are never
+ *   used as numbers.
+ */
+ress_status ress_cache_attn(const ress_cache_shape* shape, int32_t heads, int32_t tokens,
+                            const void* q, int64_t q_stride, const void* k_cache,
+                            const void* v_cache, const float* k_scale, const float* v_scale,
+                            const int32_t* table, const int32_t* lengths,
+                            const int32_t* offsets, int32_t step, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Synchronises `stream`, then reports and clears the device error flag that
