@@ -152,6 +152,24 @@ bool make_token_map(CUtensorMap* map, const void* base, const Geometry& g, int r
   return r == CUDA_SUCCESS;
 }
 
+bool make_rows_map(CUtensorMap* map, const void* base, int heads, int64_t rows,
+                   int64_t row_stride, int box_heads, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode_fn();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)rows};
+  const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)row_stride * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)kHeadDim, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    snprintf(g_last_cuda_error, sizeof(g_last_cuda_error),
+             "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return r == CUDA_SUCCESS;
+}
+
 bool make_f32_rows_map(CUtensorMap* map, const void* base, int rows, int heads,
                        size_t head_stride_bytes) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode_fn();

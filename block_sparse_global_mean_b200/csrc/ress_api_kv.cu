@@ -129,7 +129,7 @@ ress_status ress_cross_attn(const ress_cross_shape* shape, const void* q, const 
   p.k_lens = kv_lens;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  return launch_cross(g, p, workspace, static_cast<cudaStream_t>(stream));
+  return launch_cross(p, workspace, static_cast<cudaStream_t>(stream));
 }
 
 ress_status ress_cross_attn_bwd(const ress_cross_shape* shape, const void* q, const void* k,

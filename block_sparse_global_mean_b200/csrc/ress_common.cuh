@@ -96,7 +96,10 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // (RESS_ERR_TIMEOUT, `detail`) and returns false.  The first probe is inline;
 // the bounded loop is an out-of-line call, so that the many wait sites of a
 // kernel do not each carry a copy of it in the instruction stream.
-static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity,
+#ifndef RESS_WAIT_FN
+#define RESS_WAIT_FN __noinline__   // kernels that move registers between warps allow no calls
+#endif
+static __device__ RESS_WAIT_FN bool mbar_wait_slow(uint32_t bar, uint32_t parity,
                                                    volatile int* abort_flag, DeviceError* err,
                                                    int detail) {
   const unsigned long long t0 = global_timer_ns();
@@ -122,7 +125,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
 
 // Same, but ignores the abort flag (used to drain copies in flight before a
 // CTA exits).  Returns false after the time limit.
-static __device__ __noinline__ bool mbar_wait_drain_slow(uint32_t bar, uint32_t parity,
+static __device__ RESS_WAIT_FN bool mbar_wait_drain_slow(uint32_t bar, uint32_t parity,
                                                          DeviceError* err, int detail) {
   const unsigned long long t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {

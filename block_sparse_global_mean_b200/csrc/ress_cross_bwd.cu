@@ -1,5 +1,5 @@
-// Attention over keys of another length, and over the 8-bit cache: one thread
-// per query row, keys in shared memory (first, plain version).
+// Gradients of the attention over keys of another length: one thread per row,
+// partners in shared memory (first, plain version).
 #include "ress_common.cuh"
 #include "ress_internal.h"
 #include "ress_kv.h"
@@ -12,104 +12,10 @@ namespace {
 constexpr int kRowsPerCta = 128;
 constexpr int kKeys = 32;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
-}
 
 __device__ __forceinline__ void load_row(const __nv_bfloat16* src, float (&r)[64]) {
 #pragma unroll
   for (int d = 0; d < 64; ++d) r[d] = __bfloat162float(src[d]);
-}
-
-template <bool kCache>
-__global__ void __launch_bounds__(kRowsPerCta) cross_fwd_kernel(const CrossParams p) {
-  __shared__ float sk[kKeys][64], sv[kKeys][64];
-  __shared__ TileFind find;
-  __shared__ int s_ok[kKeys];
-  int b, tile;
-  if (!find_tile(p.q_off, p.seqs, p.nq, kRowsPerCta, blockIdx.x, &find, &b, &tile, p.err, 90))
-    return;
-  const int h = blockIdx.y, hk = h / p.group;
-  const SeqRange qs = seq_range(p.q_off, p.q_lens, b, p.nq, p.err, 90);
-  SeqRange ks;
-  if (kCache) {
-    int len = p.lengths[b];
-    if (len < 0 || (long long)len > (long long)p.max_pages * p.page) {
-      raise_device_error(p.err, RESS_ERR_BAD_INDEX, 94);
-      len = max(0, min(len, p.max_pages * p.page));
-    }
-    ks = SeqRange{0, len, len};
-  } else {
-    ks = seq_range(p.k_off, p.k_lens, b, p.nk, p.err, 91);
-  }
-  const int i = tile * kRowsPerCta + threadIdx.x;
-  const bool real = i < qs.valid;
-  const int row = qs.start + i;
-  float q[64], o[64], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int d = 0; d < 64; ++d) q[d] = o[d] = 0.f;
-  if (real) load_row(p.q + (size_t)row * p.q_stride + h * 64, q);
-  const int end = kCache ? step_end(ks.valid, qs.rows, i, p.step) : ks.valid;
-  for (int k0 = 0; k0 < ks.valid; k0 += kKeys) {
-    __syncthreads();
-    const int n = min(kKeys, ks.valid - k0);
-    for (int e = threadIdx.x; e < kKeys * 64; e += kRowsPerCta) {
-      const int t = e >> 6, d = e & 63, key = k0 + t;
-      float a = 0.f, c = 0.f;
-      bool ok = t < n;
-      if (ok && kCache) {
-        const int id = p.table[(size_t)b * p.max_pages + key / p.page];
-        ok = id >= 0 && id < p.pages;
-        if (!ok) raise_device_error(p.err, RESS_ERR_BAD_INDEX, 95);
-        if (ok) {
-          const size_t ph = (size_t)id * p.kv_heads + hk;
-          const size_t at = (ph * p.page + key % p.page) * 64 + d;
-          a = e4m3_value(p.k_cache[at]) * p.k_scale[ph];
-          c = e4m3_value(p.v_cache[at]) * p.v_scale[ph];
-        }
-      } else if (ok) {
-        a = __bfloat162float(p.k[(size_t)(ks.start + key) * p.k_stride + hk * 64 + d]);
-        c = __bfloat162float(p.v[(size_t)(ks.start + key) * p.v_stride + hk * 64 + d]);
-      }
-      sk[t][d] = a;
-      sv[t][d] = c;
-      if (d == 0) s_ok[t] = ok;
-    }
-    __syncthreads();
-    float s[kKeys], mx = m;
-#pragma unroll
-    for (int t = 0; t < kKeys; ++t) {
-      float acc = 0.f;
-#pragma unroll
-      for (int d = 0; d < 64; ++d) acc = fmaf(q[d], sk[t][d], acc);
-      s[t] = (s_ok[t] && k0 + t < end) ? acc * (0.125f * kLog2e) : -INFINITY;
-      mx = fmaxf(mx, s[t]);
-    }
-    if (mx == -INFINITY) continue;
-    const float alpha = exp2f(m - mx);
-    l *= alpha;
-#pragma unroll
-    for (int d = 0; d < 64; ++d) o[d] *= alpha;
-    m = mx;
-#pragma unroll
-    for (int t = 0; t < kKeys; ++t) {
-      const float pt = exp2f(s[t] - m);
-      l += pt;
-#pragma unroll
-      for (int d = 0; d < 64; ++d) o[d] = fmaf(pt, sv[t][d], o[d]);
-    }
-  }
-  if (i >= qs.rows) return;
-  const bool empty = !real || !(l > 0.f);
-  const float inv = empty ? 0.f : 1.f / l;
-  __nv_bfloat16* dst = p.out + ((size_t)row * p.heads + h) * 64;
-#pragma unroll
-  for (int d = 0; d < 64; ++d) dst[d] = __float2bfloat16(empty ? 0.f : o[d] * inv);
-  if (p.lse) p.lse[(size_t)h * p.nq + row] = empty ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // delta and dQ: one thread per query row.
@@ -234,24 +140,9 @@ unsigned tiles_of(int n, int seqs, bool packed) {
 
 }  // namespace
 
-size_t cross_workspace(const CrossGeometry&) { return 0; }
 size_t cross_bwd_workspace(const CrossGeometry& g) {
   return align256(sizeof(float) * (size_t)g.heads * g.nq);
 }
-size_t cache_attn_workspace(const ress_cache_shape&, int, int) { return 0; }
-
-ress_status launch_cross(const CrossGeometry& g, CrossParams p, void*, cudaStream_t st) {
-  const dim3 grid(tiles_of(p.nq, p.seqs, p.q_off != nullptr), g.heads);
-  cross_fwd_kernel<false><<<grid, kRowsPerCta, 0, st>>>(p);
-  return record_cuda(cudaGetLastError());
-}
-
-ress_status launch_cache_attn(CrossParams p, void*, cudaStream_t st) {
-  const dim3 grid(tiles_of(p.nq, p.seqs, true), p.heads);
-  cross_fwd_kernel<true><<<grid, kRowsPerCta, 0, st>>>(p);
-  return record_cuda(cudaGetLastError());
-}
-
 ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams p, void* ws, cudaStream_t st) {
   p.delta = static_cast<float*>(ws);
   if (p.nq > 0) {

@@ -72,6 +72,12 @@ bool make_f32_rows_map(CUtensorMap* map, const void* base, int rows, int heads,
 // of 64 (d) x 1 (head) x `rows` (tokens), 128-byte swizzle.
 bool make_token_map(CUtensorMap* map, const void* base, const Geometry& g, int rows);
 
+// Builds a 3-D TMA map over rows [rows][heads][64] of bf16, `row_stride`
+// elements apart, with a box of 64 (d) x `box_heads` x `box_rows`, 128-byte
+// swizzle; rows behind the last read as zero.
+bool make_rows_map(CUtensorMap* map, const void* base, int heads, int64_t rows,
+                   int64_t row_stride, int box_heads, int box_rows);
+
 // Records `err` as this thread's last CUDA error (for ress_last_cuda_error)
 // and returns RESS_ERR_CUDA, or RESS_OK for cudaSuccess.
 ress_status record_cuda(cudaError_t err);

@@ -58,7 +58,7 @@ struct CrossBwdParams {
 size_t cross_workspace(const CrossGeometry& g);
 size_t cross_bwd_workspace(const CrossGeometry& g);
 size_t cache_attn_workspace(const ress_cache_shape& s, int heads, int tokens);
-ress_status launch_cross(const CrossGeometry& g, CrossParams p, void* ws, cudaStream_t st);
+ress_status launch_cross(CrossParams p, void* ws, cudaStream_t st);
 ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams p, void* ws, cudaStream_t st);
 ress_status launch_cache_attn(CrossParams p, void* ws, cudaStream_t st);
 
