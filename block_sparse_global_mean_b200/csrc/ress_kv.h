@@ -49,7 +49,6 @@ struct CrossBwdParams {
   const int32_t* k_off;
   const int32_t* q_lens;
   const int32_t* k_lens;
-  float* delta;            // [heads][nq], in the workspace
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;

@@ -98,24 +98,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, ok);
 }
 
-// 2^x for a pair on the FMA and integer pipes, as exp2_poly2 but of degree 4
-// (largest relative error 2.8e-6, mean 4e-8): lse is a sum of these unrounded.
-__device__ __forceinline__ float2 exp2_poly4(float2 x) {
-  constexpr float kShift = 12582912.0f;   // 1.5 * 2^23
-  x.x = fmaxf(x.x, -126.0f);
-  x.y = fmaxf(x.y, -126.0f);
-  const float2 t = fadd2(x, make_float2(kShift, kShift));
-  const float2 n = fadd2(t, make_float2(-kShift, -kShift));
-  const float2 f = ffma2(n, make_float2(-1.0f, -1.0f), x);
-  float2 q = ffma2(make_float2(0.00957007986f, 0.00957007986f), f,
-                   make_float2(0.0559178367f, 0.0559178367f));
-  q = ffma2(q, f, make_float2(0.240247443f, 0.240247443f));
-  q = ffma2(q, f, make_float2(0.693121791f, 0.693121791f));
-  q = ffma2(q, f, make_float2(0.999999285f, 0.999999285f));
-  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
-}
-
 // Two e4m3 codes in the high bytes of each half: sign to bit 15, exponent and
 // mantissa below bf16's sign, so the half reads as 2^-120 times the code.
 __device__ __forceinline__ uint32_t code_pair(uint32_t h, __nv_bfloat162 m) {
