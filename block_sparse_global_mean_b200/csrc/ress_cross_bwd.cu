@@ -668,6 +668,10 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
     s.heads = g.kv_heads;
     s.tile_rows = dq ? p.tps : 128;
     s.mult = dq ? 1 : g.group;
+    s.row_mult = 1;
+    s.chunk = kChunk;
+    s.item_cost = kItemCost;
+    s.min_share = kMinShare;
     s.grid = kSms;
   }
   CUtensorMap tq, tdo, tqg, tdog, tk, tv;

@@ -60,6 +60,8 @@ size_t cache_attn_workspace(const ress_cache_shape& s, int heads, int tokens);
 ress_status launch_cross(CrossParams p, void* ws, cudaStream_t st);
 ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams p, void* ws, cudaStream_t st);
 ress_status launch_cache_attn(CrossParams p, void* ws, cudaStream_t st);
+size_t cache_decode_workspace();
+ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st);
 
 ress_status launch_cache_plan(const ress_cache_shape& s, const int32_t* added,
                               const int32_t* lengths, int32_t* table, const int32_t* free_pages,

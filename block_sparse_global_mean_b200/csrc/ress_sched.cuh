@@ -1,22 +1,23 @@
 // Even shares of ragged work.  An operator over packed sequences has items
-// (sequence, head, tile of rows), each a loop over chunks of 128 columns (keys,
-// or query rows in the key gradient).  The lengths live on the device, so no
-// host can plan the split.  Instead all items stand on one line of work units:
-// an item is kItemCost units (its fixed work: first loads, epilogue) and 128
-// units per chunk, CTA i owns units [i * share, (i + 1) * share), and chunk c
-// of an item belongs to the CTA that owns unit kItemCost + 128 c of it.  Items
-// cut by a share's end leave float32 partial results, which a second kernel
-// joins in the order of the chunks, so results do not depend on timing.  Long
-// items are split over many CTAs, short ones share a CTA, and one rule serves
-// one row against 140,800 keys and thousands of rows alike.
+// (sequence, head, tile of rows), each a loop over chunks of columns (keys, or
+// query rows in the key gradient).  The lengths live on the device, so no host
+// can plan the split.  Instead all items stand on one line of work units: an
+// item is item_cost units (its fixed work: first loads, epilogue) and a unit per
+// column, in whole chunks.  Worker i (a CTA; a warp over the cache's short
+// query ranges) owns units [i * share, (i + 1) * share), and chunk c of an item
+// belongs to the worker that owns its unit item_cost + chunk * c.  Items cut by a
+// share's end leave float32 partial results, which a second kernel joins in the
+// order of the chunks, so results do not depend on timing.  Long items are split
+// over many workers, short ones share one, and one rule serves one row against
+// 140,800 keys and thousands of rows alike.
 #pragma once
 
 #include "ress_seq.cuh"
 
 namespace ress {
 
-constexpr int kChunk = 128;       // columns per chunk
-constexpr int kItemCost = 256;    // an item's fixed work, in units of a column
+constexpr int kChunk = 128;       // columns per chunk of the tensor-core walks
+constexpr int kItemCost = 256;    // an item's fixed work there, in units of a column
 constexpr int kMinShare = 512;    // smallest share worth a CTA
 
 struct SchedParams {
@@ -29,10 +30,12 @@ struct SchedParams {
   int rows, cols;             // rows and columns in all
   int row_detail, col_detail; // error details of bad offsets
   int seqs, heads;
-  int tile_rows;              // sequence rows of a tile
+  int row_mult;               // item rows per sequence row
+  int tile_rows;              // item rows of a tile
   int mult;                   // passes over the columns (query heads of a key head)
-  int step;                   // the cache's step mask (0: none)
-  int grid;                   // CTAs
+  int step;                   // the cache's step mask (0: none); needs row_mult 1
+  int chunk, item_cost, min_share;
+  int grid;                   // workers
   long long max_len;          // largest valid entry of `lengths`
 };
 
@@ -62,19 +65,19 @@ struct SeqCost {
 };
 __device__ __forceinline__ SeqCost sched_cost(const SchedParams& p, const SeqRange& r,
                                               const SeqRange& c) {
-  SeqCost s{(int)(((long long)r.rows + p.tile_rows - 1) / p.tile_rows), 0, 0};
+  SeqCost s{(int)(((long long)r.rows * p.row_mult + p.tile_rows - 1) / p.tile_rows), 0, 0};
   if (p.step > 0 && p.step < r.rows) {
-    s.base = kItemCost + max(c.valid - r.rows, 0) + p.tile_rows;
+    s.base = p.item_cost + max(c.valid - r.rows, 0) + p.tile_rows;
     s.slope = p.tile_rows;
   } else {
-    s.base = kItemCost + (long long)((c.valid + kChunk - 1) / kChunk) * kChunk * p.mult;
+    s.base = p.item_cost + (long long)((c.valid + p.chunk - 1) / p.chunk) * p.chunk * p.mult;
   }
   return s;
 }
 
 // Chunks whose unit lies before unit x of an item.
-__device__ __forceinline__ long long sched_chunks_before(long long x) {
-  return x <= kItemCost ? 0 : (x - kItemCost + kChunk - 1) / kChunk;
+__device__ __forceinline__ long long sched_chunks_before(const SchedParams& p, long long x) {
+  return x <= p.item_cost ? 0 : (x - p.item_cost + p.chunk - 1) / p.chunk;
 }
 
 struct SchedShared {
@@ -128,9 +131,59 @@ __device__ __forceinline__ void sched_find(const SchedParams& p, SchedShared* sh
   __syncthreads();
 }
 
+// The same for workers that are warps: `before` (one entry per thread of the
+// CTA) gets the units before each thread's sequences, and each warp then looks
+// up its own unit.
+__device__ __forceinline__ long long sched_prefix(const SchedParams& p, long long* warp_sum,
+                                                  long long* before) {
+  const int threads = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.seqs + threads - 1) / threads;
+  const int b0 = min(p.seqs, (int)threadIdx.x * per), b1 = min(p.seqs, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const SeqCost s = sched_cost(p, sched_rows(p, b), sched_cols(p, b));
+    mine += s.before(s.tiles) * p.heads;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  long long base = 0, total = 0;
+  for (int w = 0; w < threads / 32; ++w) {
+    if (w < warp) base += warp_sum[w];
+    total += warp_sum[w];
+  }
+  before[threadIdx.x] = base + incl - mine;
+  __syncthreads();
+  return total;
+}
+// Sequence of unit u (< total) and its first unit.
+__device__ __forceinline__ void sched_locate(const SchedParams& p, const long long* before,
+                                             long long u, int* b, long long* start) {
+  const int threads = blockDim.x, lane = threadIdx.x & 31;
+  int slot = -1;   // last entry <= u that is not followed by an equal one
+  for (int i = 0; i < threads; i += 32)
+    slot += __popc(__ballot_sync(0xffffffffu, before[i + lane] <= u));
+  const int per = (p.seqs + threads - 1) / threads;
+  long long at = before[slot];
+  int s = slot * per;
+  for (; s < p.seqs; ++s) {
+    const SeqCost c = sched_cost(p, sched_rows(p, s), sched_cols(p, s));
+    const long long n = c.before(c.tiles) * p.heads;
+    if (u < at + n) break;
+    at += n;
+  }
+  *b = s;
+  *start = at;
+}
+
 __device__ __forceinline__ long long sched_share(const SchedParams& p, long long total) {
   const long long s = (total + p.grid - 1) / p.grid;
-  return s < kMinShare ? kMinShare : s;
+  return s < p.min_share ? p.min_share : s;
 }
 
 // The item at a unit of a sequence.
@@ -164,9 +217,9 @@ __device__ __forceinline__ SchedItem sched_item(const SeqCost& s, int b, long lo
   return it;
 }
 
-// What a CTA does of one item.  kind 0: nothing is left; 1: all of it (the
+// What a worker does of one item.  kind 0: nothing is left; 1: all of it (the
 // result goes to the outputs); 2: its end or middle (partial slot 0 of the
-// CTA); 3: its beginning (partial slot 1).
+// worker); 3: its beginning (partial slot 1).
 struct Segment {
   int kind;
   int b, head, tile;
@@ -197,10 +250,10 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, SchedWalk& w
     const SchedItem it = sched_item(s, w.b, w.seq_start, w.at);
     const long long x0 = w.at - it.start;
     const long long x1 = min(w.ub - it.start, it.cost);
-    long long chunks = (long long)((c.valid + kChunk - 1) / kChunk) * p.mult;
+    long long chunks = (long long)((c.valid + p.chunk - 1) / p.chunk) * p.mult;
     if (p.step > 0) {
       const int last = min((it.tile + 1) * p.tile_rows, r.rows) - 1;
-      chunks = (step_end(c.valid, r.rows, last, p.step) + kChunk - 1) / kChunk;
+      chunks = (step_end(c.valid, r.rows, last, p.step) + p.chunk - 1) / p.chunk;
     }
     g.b = w.b;
     g.head = it.head;
@@ -210,8 +263,8 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, SchedWalk& w
     g.rows_valid = r.valid;
     g.col_start = c.start;
     g.cols_valid = c.valid;
-    g.c0 = (int)min(sched_chunks_before(x0), chunks);
-    g.c1 = x1 == it.cost ? (int)chunks : (int)min(sched_chunks_before(x1), chunks);
+    g.c0 = (int)min(sched_chunks_before(p, x0), chunks);
+    g.c1 = x1 == it.cost ? (int)chunks : (int)min(sched_chunks_before(p, x1), chunks);
     g.kind = x0 > 0 ? 2 : x1 == it.cost ? 1 : 3;
     w.at = it.start + x1;
     return g;

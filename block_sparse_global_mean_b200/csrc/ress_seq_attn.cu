@@ -711,8 +711,16 @@ size_t parts_bytes(bool pair) {
 size_t cross_workspace(const CrossGeometry& g) {
   return g.nq == 0 ? 0 : parts_bytes(use_pair(g.nq, g.group, g.seqs));
 }
+// Up to 32 rows per request and key head on average, the step that adds a token
+// or a few to every request, go to the register form of ress_cache_decode.cu.
+static bool use_decode(int tokens, int group, int requests) {
+  return (long long)tokens * group <= 32ll * requests;
+}
 size_t cache_attn_workspace(const ress_cache_shape& s, int heads, int tokens) {
-  return tokens == 0 ? 0 : parts_bytes(use_pair(tokens, heads / s.kv_heads, s.requests));
+  const int group = heads / s.kv_heads;
+  if (tokens == 0) return 0;
+  return use_decode(tokens, group, s.requests) ? cache_decode_workspace()
+                                               : parts_bytes(use_pair(tokens, group, s.requests));
 }
 
 static ress_status launch_seq(const CrossParams& c, bool cache, void* ws, cudaStream_t st) {
@@ -737,6 +745,10 @@ static ress_status launch_seq(const CrossParams& c, bool cache, void* ws, cudaSt
   p.sched.seqs = c.seqs;
   p.sched.heads = c.kv_heads;
   p.sched.mult = 1;
+  p.sched.row_mult = 1;
+  p.sched.chunk = kChunk;
+  p.sched.item_cost = kItemCost;
+  p.sched.min_share = kMinShare;
   p.sched.grid = kSms;
   CUtensorMap tq, tk, tv;
   if (!make_rows_map(&tq, c.q, c.heads, c.nq, c.q_stride, c.group, p.tps)) return RESS_ERR_CUDA;
@@ -770,6 +782,7 @@ ress_status launch_cross(CrossParams p, void* ws, cudaStream_t st) {
 }
 
 ress_status launch_cache_attn(CrossParams p, void* ws, cudaStream_t st) {
+  if (use_decode(p.nq, p.group, p.seqs)) return launch_cache_decode(p, ws, st);
   return launch_seq(p, true, ws, st);
 }
 
