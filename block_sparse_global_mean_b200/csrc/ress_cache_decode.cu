@@ -55,6 +55,7 @@ struct DecodeParams {
   float* lse;
   float* part_o;       // [workers][2][16][64]
   float2* part_ml;     // [workers][2][16]
+  SplitItem* split;    // [workers]
   const uint8_t* k_cache;
   const uint8_t* v_cache;
   const float* k_scale;
@@ -65,8 +66,6 @@ struct DecodeParams {
 
 struct Smem {
   uint8_t ring[kWarps][kStages][2 * kHalf];
-  long long before[kWarps * 32];
-  long long warp_sum[32];
   uint64_t full[kWarps][kStages];
   int abort_flag;
 };
@@ -128,12 +127,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     fence_mbarrier_init();
   }
   if (threadIdx.x == 0) sm->abort_flag = 0;
-  const long long total = sched_prefix(p.sched, sm->warp_sum, sm->before);
-  const long long share = sched_share(p.sched, total);
+  allow_next_kernel();
+  __syncthreads();
   const int worker = warp * kSms + (int)blockIdx.x;   // few workers: spread over the SMs
-  SchedWalk walk{worker * share, min((worker + 1) * share, total), 0, 0};
-  if (walk.at >= total) return;
-  sched_locate(p.sched, sm->before, walk.at, &walk.b, &walk.seq_start);
+  SchedWalk walk{0, 0, 0, 0};
+  const SchedPlan plan = sched_begin(p.sched, worker, &walk);
+  SplitItem split{-1, 0, 0, 0, 0, 0, 0, 0};
 
   const int pos_mask = (1 << p.page_log2) - 1;
   uint8_t* ring = &sm->ring[warp][0][0];
@@ -146,8 +145,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int v_row0 = 2 * t + (t & 1), v_row1 = 2 * t + 1 - (t & 1);
 
   for (;;) {
-    const Segment seg = sched_next(p.sched, walk);
-    if (seg.kind == 0 || !ok) break;
+    const Segment seg = sched_next(p.sched, plan, walk);
+    if (seg.kind == 0) break;
+    if (seg.last >= 0) split = split_of(seg);
     const int rows = seg.rows * p.group;          // item rows of the request
     const int r0 = seg.tile * kRows + g, r1 = r0 + 8;
     const bool live0 = r0 < rows, live1 = r1 < rows;
@@ -378,98 +378,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
     }
   }
+  if (lane == 0) store_split(p.split + worker, split);
   // Copies still in flight (after a timeout) land before the warp leaves.
   for (; used < issued; ++used)
     mbar_wait_drain(bar + 8 * (used % kStages), (used / kStages) & 1, p.err, 181);
 }
 
-// Joins the parts of one (token, key head): its query heads are rows of one
-// item, whose parts lie with consecutive workers.  A warp takes a row: first
-// the maximum over all parts (a part per lane), then the weighted sum.
-__global__ void __launch_bounds__(256) cache_decode_combine_kernel(const __grid_constant__ DecodeParams p) {
-  __shared__ SchedShared sh;
-  __shared__ int s_b;
-  __shared__ long long s_part[8], s_total[8];
-  const int tok = (int)blockIdx.x, hk = (int)blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // The request of the token, and the units before and in all.
-  if (threadIdx.x == 0) s_b = -1;
-  __syncthreads();
-  for (int b = threadIdx.x; b < p.sched.seqs; b += 256) {
-    const SeqRange r = sched_rows(p.sched, b);
-    if (tok >= r.start && tok < r.start + r.rows) atomicMax(&s_b, b);
-  }
-  __syncthreads();
-  const int b = s_b;
-  if (b < 0) return;
-  long long before = 0, total = 0;
-  for (int i = threadIdx.x; i < p.sched.seqs; i += 256) {
-    const SeqCost s = sched_cost(p.sched, sched_rows(p.sched, i), sched_cols(p.sched, i));
-    const long long n = s.before(s.tiles) * p.sched.heads;
-    total += n;
-    if (i < b) before += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-  }
-  if (lane == 0) s_part[warp] = before, s_total[warp] = total;
-  __syncthreads();
-  before = total = 0;
-  for (int w = 0; w < 8; ++w) before += s_part[w], total += s_total[w];
-  const long long share = sched_share(p.sched, total);
-  const SeqRange rs = sched_rows(p.sched, b);
-  const SeqCost cost = sched_cost(p.sched, rs, sched_cols(p.sched, b));
-
-  for (int h = warp; h < p.group; h += 8) {
-    const int r = (tok - rs.start) * p.group + h;
-    const int tile = r / kRows, rr = r % kRows;
-    const long long start = before + hk * cost.before(cost.tiles) + cost.before(tile);
-    const int w0 = (int)(start / share), w1 = (int)((start + cost.base - 1) / share);
-    if (w0 == w1) continue;   // written by its only worker
-    auto part_of = [&](int w) {
-      // The worker in which the item starts has it in slot 1, the others in slot 0.
-      return ((size_t)w * 2 + (w == w0 ? 1 : 0)) * kRows + rr;
-    };
-    float m = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32) m = fmaxf(m, p.part_ml[part_of(w)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
-    float2 o = make_float2(0.f, 0.f);
-    for (int wb = w0; wb <= w1; wb += 32) {
-      float f = 0.f;
-      if (wb + lane <= w1) {
-        const float2 ml = p.part_ml[part_of(wb + lane)];
-        f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
-        l = fmaf(f, ml.y, l);
-      }
-      const int n = min(32, w1 - wb + 1);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float2 x = reinterpret_cast<const float2*>(p.part_o + part_of(wb + i) * kHeadDim)[lane];
-        o.x = fmaf(fi, x.x, o.x);
-        o.y = fmaf(fi, x.y, o.y);
-      }
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    const bool empty = m == -INFINITY;
-    const float inv = empty ? 0.f : 1.0f / l;
-    const int head = hk * p.group + h;
-    reinterpret_cast<uint32_t*>(p.out + ((size_t)tok * p.heads + head) * kHeadDim)[lane] =
-        pack_bf16x2(o.x * inv, o.y * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(size_t)head * p.nq + tok] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
-  }
+// Joins the parts of the item that worker blockIdx.x began and did not end.
+__global__ void __launch_bounds__(256)
+    cache_decode_combine_kernel(const __grid_constant__ DecodeParams p) {
+  wait_for_previous_kernel();
+  const SplitItem it = load_split(p.split + blockIdx.x);
+  if (it.head < 0) return;
+  auto token_of = [&](int r) { return (size_t)(it.row_start + (it.tile * kRows + r) / p.group); };
+  auto head_of = [&](int r) { return it.head * p.group + (it.tile * kRows + r) % p.group; };
+  join_item<8>(
+      it, (int)blockIdx.x, p.part_ml, p.part_o, kRows, min(kRows, it.rows * p.group - it.tile * kRows),
+      [&](int r) -> __nv_bfloat16* {
+        return p.out + (token_of(r) * p.heads + head_of(r)) * kHeadDim;
+      },
+      [&](int r) -> float* {
+        return p.lse ? p.lse + (size_t)head_of(r) * p.nq + token_of(r) : nullptr;
+      });
 }
 
 }  // namespace
 
 size_t cache_decode_workspace() {
-  return align256((size_t)kWorkers * 2 * kRows * (kHeadDim * sizeof(float) + sizeof(float2)));
+  return align256((size_t)kWorkers * (2 * kRows * (kHeadDim * sizeof(float) + sizeof(float2)) +
+                                      sizeof(SplitItem)));
 }
 
 ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st) {
@@ -485,6 +422,7 @@ ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st)
   p.lse = c.lse;
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)kWorkers * 2 * kRows * kHeadDim);
+  p.split = reinterpret_cast<SplitItem*>(p.part_ml + (size_t)kWorkers * 2 * kRows);
   p.k_cache = c.k_cache;
   p.v_cache = c.v_cache;
   p.k_scale = c.k_scale;
@@ -514,8 +452,8 @@ ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st)
     return s;
   cache_decode_kernel<<<kSms, kWarps * 32, kSmem, st>>>(p);
   if (ress_status s = record_cuda(cudaGetLastError())) return s;
-  cache_decode_combine_kernel<<<dim3((unsigned)c.nq, (unsigned)c.kv_heads), 256, 0, st>>>(p);
-  return record_cuda(cudaGetLastError());
+  return record_cuda(
+      launch_dependent(cache_decode_combine_kernel, dim3(kWorkers), dim3(256), st, p));
 }
 
 }  // namespace ress

@@ -58,6 +58,7 @@ struct BwdParams {
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   float* part[2];            // [grid][2][128 rows][128 (key walk) or 64]
+  SplitItem* split;          // [2 walks][grid]
 };
 
 struct __align__(16) Ctl {
@@ -75,7 +76,6 @@ struct __align__(16) Ctl {
   uint32_t tmem_base;
   int abort_flag;
   Segment seg[2];
-  SchedShared sched;
 };
 constexpr size_t kSmem = 1024 + 2 * kTileBytes + kStages * kStageBytes + sizeof(Ctl);
 static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -159,17 +159,20 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
     tmem_alloc(smem_addr(&ctl->tmem_base), kTmemCols);
     tmem_relinquish();
   }
+  if (threadIdx.x == 96) {
+    tma_prefetch_desc(tm_a1);
+    tma_prefetch_desc(tm_a2);
+    tma_prefetch_desc(tm_b1);
+    tma_prefetch_desc(tm_b2);
+  }
   SchedWalk walk{0, 0, 0, 0};
-  sched_find(sp, &ctl->sched, [&](long long total) {
-    const long long share = sched_share(sp, total);
-    walk.at = blockIdx.x * share;
-    walk.ub = min(walk.at + share, total);
-    return walk.at;
-  });
-  walk.b = ctl->sched.b;
-  walk.seq_start = ctl->sched.start;
-  if (walk.b < 0) walk.at = walk.ub;
-  if (threadIdx.x == 64) ctl->seg[0] = sched_next(sp, walk);
+  SchedPlan plan;
+  if (warp == 2) {
+    plan = sched_begin(sp, (int)blockIdx.x, &walk);
+    if (lane == 0) ctl->seg[0] = sched_next(sp, plan, walk);
+  }
+  wait_for_previous_kernel();   // delta
+  allow_next_kernel();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -337,10 +340,14 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
     } else {
       // ---------------- the next item (warp 2); lse and delta of a chunk (warp 3) ----------------
       int kc = 0;
+      SplitItem split{-1, 0, 0, 0, 0, 0, 0, 0};
       for (int s = 0;; ++s) {
         const Segment& g = ctl->seg[s & 1];
         if (g.kind == 0) break;
-        if (threadIdx.x == 64) ctl->seg[(s + 1) & 1] = sched_next(sp, walk);
+        if (threadIdx.x == 64) {
+          if (g.last >= 0) split = split_of(g);
+          ctl->seg[(s + 1) & 1] = sched_next(sp, plan, walk);
+        }
         if (!kDQ && warp == 3) {
           for (int c = g.c0; c < g.c1; ++c, ++kc) {
             const int st = kc % kStages;
@@ -369,6 +376,7 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
         __syncwarp();
         if (!end_of_item()) break;
       }
+      if (threadIdx.x == 64) store_split(p.split + (kDQ ? kSms : 0) + blockIdx.x, split);
     }
   } else {
     // ---------------- P, dS and the epilogue ----------------
@@ -580,27 +588,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Adds the parts of the items that were cut (see ress_sched.cuh) in the order
-// of their chunks: blockIdx.z the walk, one warp per row.
-__global__ void __launch_bounds__(256) cross_bwd_combine_kernel(const __grid_constant__ BwdParams p) {
-  __shared__ SchedShared sh;
-  const bool dq = blockIdx.z == 1;
+// of their chunks: blockIdx.y the walk, one warp per row at a time.
+__global__ void __launch_bounds__(1024)
+    cross_bwd_combine_kernel(const __grid_constant__ BwdParams p) {
+  const bool dq = blockIdx.y == 1;
   const SchedParams& sp = p.sched[dq ? 1 : 0];
-  const SplitItem it = sched_split_item(sp, &sh, (int)blockIdx.x);
+  const int first = (int)blockIdx.x;
+  wait_for_previous_kernel();
+  const SplitItem it = load_split(p.split + (dq ? kSms : 0) + first);
   if (it.head < 0) return;
-  const SeqRange rs = sched_rows(sp, it.b);
   const int lane = threadIdx.x & 31;
   const int width = dq ? 64 : 128;
-  for (int rr = (int)blockIdx.y * 32 + (threadIdx.x >> 5); rr < (int)blockIdx.y * 32 + 32; rr += 8) {
+  for (int rr = threadIdx.x >> 5; rr < 128; rr += 32) {
     const int tok = it.tile * sp.tile_rows + (dq ? rr / p.group : rr);
-    if ((dq && rr >= p.tps * p.group) || tok >= rs.rows) continue;
+    if ((dq && rr >= p.tps * p.group) || tok >= it.rows) continue;
     float2 a = make_float2(0.f, 0.f), b = make_float2(0.f, 0.f);
-    for (int cta = (int)blockIdx.x; cta <= it.last_cta; ++cta) {
-      const size_t part = ((size_t)cta * 2 + (cta == (int)blockIdx.x ? 1 : 0)) * 128 + rr;
+#pragma unroll 4
+    for (int w = first; w <= it.last; ++w) {
+      const size_t part = ((size_t)w * 2 + (w == first ? it.slot : 0)) * 128 + rr;
       const float2* src = reinterpret_cast<const float2*>(p.part[dq ? 1 : 0] + part * width);
       a = fadd2(a, src[lane]);
       if (!dq) b = fadd2(b, src[32 + lane]);
     }
-    const size_t row = (size_t)(rs.start + tok);
+    const size_t row = (size_t)(it.row_start + tok);
     if (dq) {
       const int head = it.head * p.group + rr % p.group;
       reinterpret_cast<uint32_t*>(p.dq + (row * p.heads + head) * kHeadDim)[lane] =
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(256) cross_bwd_combine_kernel(const __grid_con
 }
 
 struct BwdLayout {
-  size_t nl, nd, part_k, part_q, total;
+  size_t nl, nd, part_k, part_q, split, total;
 };
 BwdLayout bwd_layout(const CrossGeometry& g) {
   BwdLayout l{};
@@ -623,7 +633,8 @@ BwdLayout bwd_layout(const CrossGeometry& g) {
   l.nd = rows;
   l.part_k = 2 * rows;
   l.part_q = l.part_k + part * 128;
-  l.total = align256(l.part_q + part * 64);
+  l.split = l.part_q + part * 64;
+  l.total = align256(l.split + 2 * kSms * sizeof(SplitItem));
   return l;
 }
 
@@ -652,6 +663,7 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
   p.dv = c.dv;
   p.part[0] = reinterpret_cast<float*>(base + lay.part_k);
   p.part[1] = reinterpret_cast<float*>(base + lay.part_q);
+  p.split = reinterpret_cast<SplitItem*>(base + lay.split);
   for (int w = 0; w < 2; ++w) {
     SchedParams& s = p.sched[w];
     const bool dq = w == 1;
@@ -696,10 +708,20 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
   if (ress_status e = record_cuda(cudaFuncSetAttribute(
           cross_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)))
     return e;
-  cross_bwd_kernel<<<dim3(kSms, 2), kThreads, kSmem, st>>>(tq, tdo, tqg, tdog, tk, tv, p);
-  if (ress_status e = record_cuda(cudaGetLastError())) return e;
-  cross_bwd_combine_kernel<<<dim3(kSms, 4, 2), 256, 0, st>>>(p);
-  return record_cuda(cudaGetLastError());
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kSms, 2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = g.nq > 0 ? 1 : 0;   // behind cross_delta_kernel
+  if (ress_status e = record_cuda(
+          cudaLaunchKernelEx(&cfg, cross_bwd_kernel, tq, tdo, tqg, tdog, tk, tv, p)))
+    return e;
+  return record_cuda(launch_dependent(cross_bwd_combine_kernel, dim3(kSms, 2), dim3(1024), st, p));
 }
 
 }  // namespace ress

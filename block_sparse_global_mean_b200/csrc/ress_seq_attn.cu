@@ -65,6 +65,7 @@ struct SeqAttnParams {
   float* lse;
   float* part_o;     // [grid][2][rows][64]
   float2* part_ml;   // [grid][2][rows]: maximum (log2 domain), sum
+  SplitItem* split;  // [grid]
   // The cache.
   const uint8_t* k_cache;
   const uint8_t* v_cache;
@@ -87,7 +88,6 @@ struct __align__(8) Ctl {
   int abort_flag;
   int page_ok[kMaxStages][2];   // cache: the 64-key halves of a stage come from a page of the pool
   Segment seg[2];
-  SchedShared sched;
   float odd_m[128];
   float odd_l[128];
 };
@@ -206,17 +206,20 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
     tmem_alloc(smem_addr(&ctl->tmem_base), kTmemCols);
     tmem_relinquish();
   }
+  if (threadIdx.x == 96) {
+    tma_prefetch_desc(&tm_q);
+    if (!kCache) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+  }
+  allow_next_kernel();
   SchedWalk walk{0, 0, 0, 0};
-  sched_find(p.sched, &ctl->sched, [&](long long total) {
-    const long long share = sched_share(p.sched, total);
-    walk.at = blockIdx.x * share;
-    walk.ub = min(walk.at + share, total);
-    return walk.at;
-  });
-  walk.b = ctl->sched.b;
-  walk.seq_start = ctl->sched.start;
-  if (walk.b < 0) walk.at = walk.ub;   // nothing for this CTA
-  if (threadIdx.x == 64) ctl->seg[0] = sched_next(p.sched, walk);
+  SchedPlan plan;
+  if (warp == 2) {
+    plan = sched_begin(p.sched, (int)blockIdx.x, &walk);
+    if (lane == 0) ctl->seg[0] = sched_next(p.sched, plan, walk);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -348,11 +351,17 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
       __syncwarp();
     } else {
       // ---------------- the next item ----------------
+      SplitItem split{-1, 0, 0, 0, 0, 0, 0, 0};
       for (int s = 0;; ++s) {
-        if (ctl->seg[s & 1].kind == 0) break;
-        if (threadIdx.x == 64) ctl->seg[(s + 1) & 1] = sched_next(p.sched, walk);
+        const Segment& g = ctl->seg[s & 1];
+        if (g.kind == 0) break;
+        if (threadIdx.x == 64) {
+          if (g.last >= 0) split = split_of(g);
+          ctl->seg[(s + 1) & 1] = sched_next(p.sched, plan, walk);
+        }
         if (!end_of_item()) break;
       }
+      if (threadIdx.x == 64) store_split(p.split + blockIdx.x, split);
     }
   } else if (warp < 12) {
     // ---------------- softmax and epilogue ----------------
@@ -643,43 +652,28 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
 }
 
 // Joins the parts of the item that CTA blockIdx.x of the kernel above began
-// and did not end: parts (cta, 1), (cta + 1, 0), ... in the order of the keys.
-// One warp per row, two dimensions per lane.
+// and did not end.
 template <bool kPair>
-__global__ void __launch_bounds__(256) seq_combine_kernel(const SeqAttnParams p) {
+__global__ void __launch_bounds__(1024) seq_combine_kernel(const __grid_constant__ SeqAttnParams p) {
   constexpr int kRows = kPair ? 256 : 128;
-  __shared__ SchedShared sh;
-  const SplitItem it = sched_split_item(p.sched, &sh, (int)blockIdx.x);
+  wait_for_previous_kernel();
+  const SplitItem it = load_split(p.split + blockIdx.x);
   if (it.head < 0) return;
-  const SeqRange qs = sched_rows(p.sched, it.b);
-  const int lane = threadIdx.x & 31;
-  for (int r = (int)blockIdx.y * 32 + (threadIdx.x >> 5); r < (int)blockIdx.y * 32 + 32; r += 8) {
-    const int sub = r >> 7, rr = r & 127;
-    const int tok = it.tile * p.sched.tile_rows + sub * p.tps + rr / p.group;
-    if (rr >= p.tps * p.group || tok >= qs.rows) continue;
-    float m = -INFINITY, l = 0.f;
-    float2 o = make_float2(0.f, 0.f);
-    for (int cta = (int)blockIdx.x; cta <= it.last_cta; ++cta) {
-      const size_t part = ((size_t)cta * 2 + (cta == (int)blockIdx.x ? 1 : 0)) * kRows + r;
-      const float2 ml = p.part_ml[part];
-      if (ml.x == -INFINITY) continue;   // no key of the row in this part: its O was not written
-      const float2 x = reinterpret_cast<const float2*>(p.part_o + part * kHeadDim)[lane];
-      const float mn = fmaxf(m, ml.x);
-      const float a = fast_exp2(m - mn), c = fast_exp2(ml.x - mn);
-      l = fmaf(c, ml.y, a * l);
-      o.x = fmaf(c, x.x, a * o.x);
-      o.y = fmaf(c, x.y, a * o.y);
-      m = mn;
-    }
-    const size_t row = (size_t)(qs.start + tok);
-    const int head = it.head * p.group + rr % p.group;
-    const bool empty = m == -INFINITY;
-    const float inv = empty ? 0.f : 1.0f / l;
-    reinterpret_cast<uint32_t*>(p.out + (row * p.heads + head) * kHeadDim)[lane] =
-        pack_bf16x2(o.x * inv, o.y * inv);
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[(size_t)head * p.nq + row] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
-  }
+  auto token_of = [&](int r) { return it.tile * p.sched.tile_rows + (r >> 7) * p.tps + (r & 127) / p.group; };
+  auto head_of = [&](int r) { return it.head * p.group + (r & 127) % p.group; };
+  const int left = it.rows - it.tile * p.sched.tile_rows;   // tokens of the tile and behind it
+  const int n = left >= p.sched.tile_rows ? kRows
+                : left > p.tps                ? 128 + (left - p.tps) * p.group
+                                              : left * p.group;
+  join_item<32>(
+      it, (int)blockIdx.x, p.part_ml, p.part_o, kRows, n,
+      [&](int r) -> __nv_bfloat16* {
+        if ((r & 127) >= p.tps * p.group) return nullptr;
+        return p.out + ((size_t)(it.row_start + token_of(r)) * p.heads + head_of(r)) * kHeadDim;
+      },
+      [&](int r) -> float* {
+        return p.lse ? p.lse + (size_t)head_of(r) * p.nq + it.row_start + token_of(r) : nullptr;
+      });
 }
 
 bool use_pair(int nq, int group, int seqs) { return (long long)nq * group > 128ll * seqs; }
@@ -693,17 +687,18 @@ ress_status launch_seq_typed(const CUtensorMap& tq, const CUtensorMap& tk, const
   p.sched.tile_rows = p.tps * (kPair ? 2 : 1);
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)kSms * 2 * C::rows * kHeadDim);
+  p.split = reinterpret_cast<SplitItem*>(p.part_ml + (size_t)kSms * 2 * C::rows);
   if (ress_status s = record_cuda(cudaFuncSetAttribute(
           seq_attn_kernel<kPair, kCache>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
     return s;
   seq_attn_kernel<kPair, kCache><<<kSms, C::threads, smem, st>>>(tq, tk, tv, p);
   if (ress_status s = record_cuda(cudaGetLastError())) return s;
-  seq_combine_kernel<kPair><<<dim3(kSms, C::rows / 32), 256, 0, st>>>(p);
-  return record_cuda(cudaGetLastError());
+  return record_cuda(launch_dependent(seq_combine_kernel<kPair>, dim3(kSms), dim3(1024), st, p));
 }
 
 size_t parts_bytes(bool pair) {
-  return align256((size_t)kSms * 2 * (pair ? 256 : 128) * (kHeadDim * sizeof(float) + sizeof(float2)));
+  return align256((size_t)kSms * 2 * (pair ? 256 : 128) * (kHeadDim * sizeof(float) + sizeof(float2)) +
+                  kSms * sizeof(SplitItem));
 }
 
 }  // namespace
