@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   allow_next_kernel();
   __syncthreads();
   const int worker = warp * kSms + (int)blockIdx.x;   // few workers: spread over the SMs
-  SchedWalk walk{0, 0, 0, 0};
+  SchedWalk walk{0, 0, 0, 0, 0};
   const SchedPlan plan = sched_begin(p.sched, worker, &walk);
-  SplitItem split{-1, 0, 0, 0, 0, 0, 0, 0};
+  SplitItem split = no_split();
 
   const int pos_mask = (1 << p.page_log2) - 1;
   uint8_t* ring = &sm->ring[warp][0][0];
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (;;) {
     const Segment seg = sched_next(p.sched, plan, walk);
     if (seg.kind == 0) break;
-    if (seg.last >= 0) split = split_of(seg);
+    if (seg.parts > 0) split = split_of(seg);
     const int rows = seg.rows * p.group;          // item rows of the request
     const int r0 = seg.tile * kRows + g, r1 = r0 + 8;
     const bool live0 = r0 < rows, live1 = r1 < rows;
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (t == 0 && p.lse != nullptr)
           p.lse[(size_t)head * p.nq + row] = empty ? -INFINITY : (m + __log2f(l)) * kLn2;
       } else {
-        const size_t part = ((size_t)worker * 2 + (seg.kind == 3 ? 1 : 0)) * kRows + g + 8 * half;
+        const size_t part = ((size_t)worker * 2 + seg.slot) * kRows + g + 8 * half;
         float4* dst = reinterpret_cast<float4*>(p.part_o + part * kHeadDim + 16 * t);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(256)
   if (it.head < 0) return;
   auto token_of = [&](int r) { return (size_t)(it.row_start + (it.tile * kRows + r) / p.group); };
   auto head_of = [&](int r) { return it.head * p.group + (it.tile * kRows + r) % p.group; };
-  join_item<8>(
-      it, (int)blockIdx.x, p.part_ml, p.part_o, kRows, min(kRows, it.rows * p.group - it.tile * kRows),
+  join_item<16>(
+      it, (int)blockIdx.x, p.sched.grid, p.part_ml, p.part_o, kRows, 0, min(kRows, it.rows * p.group - it.tile * kRows),
       [&](int r) -> __nv_bfloat16* {
         return p.out + (token_of(r) * p.heads + head_of(r)) * kHeadDim;
       },

@@ -165,7 +165,7 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
     tma_prefetch_desc(tm_b1);
     tma_prefetch_desc(tm_b2);
   }
-  SchedWalk walk{0, 0, 0, 0};
+  SchedWalk walk{0, 0, 0, 0, 0};
   SchedPlan plan;
   if (warp == 2) {
     plan = sched_begin(sp, (int)blockIdx.x, &walk);
@@ -340,12 +340,12 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
     } else {
       // ---------------- the next item (warp 2); lse and delta of a chunk (warp 3) ----------------
       int kc = 0;
-      SplitItem split{-1, 0, 0, 0, 0, 0, 0, 0};
+      SplitItem split = no_split();
       for (int s = 0;; ++s) {
         const Segment& g = ctl->seg[s & 1];
         if (g.kind == 0) break;
         if (threadIdx.x == 64) {
-          if (g.last >= 0) split = split_of(g);
+          if (g.parts > 0) split = split_of(g);
           ctl->seg[(s + 1) & 1] = sched_next(sp, plan, walk);
         }
         if (!kDQ && warp == 3) {
@@ -523,7 +523,7 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
         // group half of dQ.
         constexpr int kHalves = kDQ ? 1 : 2;
         const bool scaled = kDQ || par == 1;
-        const size_t part = ((size_t)blockIdx.x * 2 + (kind == 3 ? 1 : 0)) * 128 + rr;
+        const size_t part = ((size_t)blockIdx.x * 2 + g.slot) * 128 + rr;
         const uint32_t tAcc = tmem + lane_off + (kDQ ? kColA2 + 32u * (uint32_t)par
                                                      : par == 0 ? kColA1 : kColA2);
 #pragma unroll
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Adds the parts of the items that were cut (see ress_sched.cuh) in the order
 // of their chunks: blockIdx.y the walk, one warp per row at a time.
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(256)
     cross_bwd_combine_kernel(const __grid_constant__ BwdParams p) {
   const bool dq = blockIdx.y == 1;
   const SchedParams& sp = p.sched[dq ? 1 : 0];
@@ -599,13 +599,13 @@ __global__ void __launch_bounds__(1024)
   if (it.head < 0) return;
   const int lane = threadIdx.x & 31;
   const int width = dq ? 64 : 128;
-  for (int rr = threadIdx.x >> 5; rr < 128; rr += 32) {
+  for (int rr = (int)blockIdx.z * 32 + (threadIdx.x >> 5); rr < (int)blockIdx.z * 32 + 32; rr += 8) {
     const int tok = it.tile * sp.tile_rows + (dq ? rr / p.group : rr);
     if ((dq && rr >= p.tps * p.group) || tok >= it.rows) continue;
     float2 a = make_float2(0.f, 0.f), b = make_float2(0.f, 0.f);
 #pragma unroll 4
-    for (int w = first; w <= it.last; ++w) {
-      const size_t part = ((size_t)w * 2 + (w == first ? it.slot : 0)) * 128 + rr;
+    for (int k = 0; k < it.parts; ++k) {
+      const size_t part = part_slot(it, first, sp.grid, k) * 128 + rr;
       const float2* src = reinterpret_cast<const float2*>(p.part[dq ? 1 : 0] + part * width);
       a = fadd2(a, src[lane]);
       if (!dq) b = fadd2(b, src[32 + lane]);
@@ -721,7 +721,7 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
   if (ress_status e = record_cuda(
           cudaLaunchKernelEx(&cfg, cross_bwd_kernel, tq, tdo, tqg, tdog, tk, tv, p)))
     return e;
-  return record_cuda(launch_dependent(cross_bwd_combine_kernel, dim3(kSms, 2), dim3(1024), st, p));
+  return record_cuda(launch_dependent(cross_bwd_combine_kernel, dim3(kSms, 2, 4), dim3(256), st, p));
 }
 
 }  // namespace ress

@@ -6,12 +6,19 @@
 // per column, in whole chunks.  A worker is a CTA (a warp over the cache's short
 // query ranges).
 //
-// Few items (at most half the workers), where latency counts: an item is cut
-// into equal pieces, as many as its cost asks for, and a worker does one piece.
-// More items: they stand on one line of units, and worker i owns units [i *
-// share, (i + 1) * share): chunk c of an item belongs to the worker that owns
-// its unit item_cost + chunk * c.  Long items spread over many workers, short
-// ones share one.
+// Three ways, chosen from the items' number and costs:
+//   rounds  All items cost the same: each is cut into ns equal pieces, and worker w
+//           does pieces w, w + grid, ... of (piece 0 of every item, piece 1 of every
+//           item, ...).  Workers then read the same columns of all heads and tiles
+//           at the same time, so each column comes from memory once (one view
+//           against 100 padded ones: 0.58 GB instead of 3.4 GB).
+//   pieces  Few items (at most half the workers) of several costs and little work,
+//           where latency counts: an item in as many pieces as its cost asks for,
+//           a worker does one piece.
+//   line    Otherwise: the items stand on one line of units, and worker i owns units
+//           [i * share, (i + 1) * share): chunk c of an item belongs to the worker
+//           that owns its unit item_cost + chunk * c.  Long items spread over many
+//           workers, short ones share one.
 //
 // Items that several workers touch leave float32 partial results, which a second
 // kernel joins in the order of the chunks, so results do not depend on timing.
@@ -100,9 +107,11 @@ __device__ __forceinline__ int SeqCost::pieces(long long share) const {
   return (int)div_pos(most() + share - 1, share);
 }
 
+enum SchedMode { kLine, kPieces, kRounds };
 struct SchedPlan {
-  bool pieces;        // which of the two ways
-  long long share;
+  SchedMode mode;
+  long long share;    // line, pieces: units of a worker, of a piece
+  int items, ns;      // rounds
 };
 
 __device__ __forceinline__ long long warp_sum(long long x) {
@@ -114,51 +123,112 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 // A worker's way through its items, one call of sched_next per item.
 struct SchedWalk {
   long long at, ub, seq_start;   // next unit (or piece), end, first one of sequence b
-  int b;
+  int b, worker;
 };
+
+// Pieces of the sequences from `b0` on, one per lane.
+__device__ __forceinline__ long long sched_count(const SchedParams& p, const SeqCost& cost,
+                                                 SchedMode mode, long long share) {
+  if (cost.tiles == 0) return 0;
+  const long long n = (long long)cost.tiles * p.heads;
+  return mode == kLine     ? cost.before(cost.tiles) * p.heads
+         : mode == kPieces ? n * cost.pieces(share)
+                           : n;
+}
 
 // The plan, and where `worker` begins (at == ub: nowhere).  Called by a warp.
 __device__ __forceinline__ SchedPlan sched_begin(const SchedParams& p, int worker, SchedWalk* walk) {
   const int lane = threadIdx.x & 31;
   SeqCost cost{0, 0, 0};
-  long long units = 0, items = 0, most = 0;
+  long long units = 0, items = 0, cap = 0, least = 0x7fffffffffffffffll, most = 0;
+  bool flat = true;
   for (int b = lane; b < p.seqs; b += 32) {
     cost = sched_cost(p, b);
     const long long n = (long long)cost.tiles * p.heads;
     items += n;
-    most += n * cost.most();
     units += cost.before(cost.tiles) * p.heads;
+    cap += n * cost.most();
+    if (n > 0) {
+      least = min(least, cost.base);
+      most = max(most, cost.base);
+      flat = flat && cost.slope == 0;
+    }
   }
   items = warp_sum(items);
-  SchedPlan plan;
-  plan.pieces = 2 * items <= p.grid;
-  // Pieces: every item in ceil(cost / share), at most grid in all.
-  units = warp_sum(plan.pieces ? most : units);
-  const long long workers = plan.pieces ? p.grid - items : p.grid;
-  plan.share = max(div_pos(units + workers - 1, workers), (long long)p.min_share);
-  walk->at = plan.pieces ? worker : worker * plan.share;
-  walk->ub = walk->at;
+  units = warp_sum(units);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  flat = __all_sync(0xffffffffu, flat) && least == most;
+  walk->worker = worker;
+  walk->at = walk->ub = 0;
+  SchedPlan plan{kLine, max(div_pos(units + p.grid - 1, p.grid), (long long)p.min_share),
+                 (int)min(items, 0x7fffffffll), 1};
+  if (items == 0) return plan;
+  if (flat && p.seqs <= 32 && items < (1 << 24)) {   // (sched_next looks through the sequences)
+    // Each lane tries a number of pieces: 1 .. 30, and those that fill one or
+    // two rounds.  More than two rounds only of whole items (a worker has two
+    // partial slots).
+    const int n = (int)items, chunks = (int)min(div_pos(most - p.item_cost, p.chunk), 1ll << 24);
+    int ns = lane < 30 ? lane + 1 : (lane - 29) * p.grid / n;
+    ns = max(1, min(ns, chunks));
+    const int rounds = (int)div_pos((long long)n * ns + p.grid - 1, p.grid);
+    long long t = (long long)rounds * (p.item_cost + (long long)((chunks + ns - 1) / ns) * p.chunk);
+    if (ns > 1 && rounds > 2) t = 0x7fffffffffffffll;
+    long long best = (t << 8) + ns % 256;   // the fewest pieces of the shortest
+    if (ns > 255) best = (t << 8) + 255;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
+    // The line costs an item's fixed work more, and is fully even.
+    if ((best >> 8) <= plan.share + (plan.share >> 4) + p.item_cost) {
+      const unsigned who =
+          __ballot_sync(0xffffffffu, (t << 8) + (ns > 255 ? 255 : ns) == best);
+      plan.ns = __shfl_sync(0xffffffffu, ns, __ffs((int)who) - 1);
+      plan.mode = kRounds;
+    }
+  }
+  if (plan.mode != kRounds && 2 * items <= p.grid && units <= (long long)p.grid * 16 * p.chunk) {
+    // Shares that grow until all pieces fit.  sum ceil(cost / share) <= sum cost /
+    // share + items, so the last one is sure to.
+    plan.mode = kPieces;
+    cap = warp_sum(cap);
+    for (int i = 0; i < 3; ++i) {
+      long long n = 0;
+      for (int b = lane; b < p.seqs; b += 32) {
+        if (p.seqs > 32) cost = sched_cost(p, b);
+        n += sched_count(p, cost, kPieces, plan.share);
+      }
+      if (warp_sum(n) <= p.grid) break;
+      plan.share = i < 2 ? plan.share + (plan.share >> 2)
+                         : max(plan.share, div_pos(cap + p.grid - items - 1, p.grid - items));
+    }
+  }
+  const long long unit = plan.mode == kLine ? worker * plan.share : worker;
+  if (plan.mode == kRounds) {
+    walk->at = unit;
+    walk->ub = items * plan.ns;
+    return plan;
+  }
   long long base = 0;
   for (int b0 = 0; b0 < p.seqs; b0 += 32) {
     const int b = b0 + lane;
     if (p.seqs > 32 && b < p.seqs) cost = sched_cost(p, b);
-    long long n = 0;
-    if (b < p.seqs && cost.tiles > 0)
-      n = plan.pieces ? (long long)cost.tiles * p.heads * cost.pieces(plan.share)
-                      : cost.before(cost.tiles) * p.heads;
+    const long long n = b < p.seqs ? sched_count(p, cost, plan.mode, plan.share) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const unsigned behind = __ballot_sync(0xffffffffu, base + incl > walk->at);
+    const unsigned behind = __ballot_sync(0xffffffffu, base + incl > unit);
     if (behind != 0) {
       const int l = __ffs((int)behind) - 1;
       walk->b = b0 + l;
       walk->seq_start = base + __shfl_sync(0xffffffffu, incl - n, l);
-      // The walk ends with the work; without pieces it may go on behind this batch.
-      walk->ub = plan.pieces ? walk->at + 1 : min(walk->at + plan.share, units);
+      walk->at = unit;
+      walk->ub = plan.mode == kLine ? min(unit + plan.share, units) : unit + 1;
       break;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
@@ -197,15 +267,14 @@ __device__ __forceinline__ SchedItem sched_item(const SeqCost& s, long long seq_
 }
 
 // What a worker does of one item.  kind 0: nothing is left; 1: all of it (the
-// result goes to the outputs); 2: a piece, or an end or middle (partial slot 0
-// of the worker); 3: a beginning on the line (partial slot 1).
+// result goes to the outputs); 2: a part, to the worker's partial slot `slot`.
 struct Segment {
-  int kind;
+  int kind, slot;
   int b, head, tile;
   int row_start, rows, rows_valid;
   int col_start, cols_valid;
   int c0, c1;              // chunks
-  int last;                // of the worker with the item's first part: who has its last (else -1)
+  int parts, stride;       // of an item's first part: its parts, and from one to the next
 };
 
 __device__ __forceinline__ long long sched_chunks(const SchedParams& p, const SeqRange& r,
@@ -217,27 +286,50 @@ __device__ __forceinline__ long long sched_chunks(const SchedParams& p, const Se
   return (long long)((c.valid + p.chunk - 1) / p.chunk) * p.mult;
 }
 
+// Piece `piece` of `ns` of an item's chunks.
+__device__ __forceinline__ void sched_piece(Segment& g, long long chunks, int piece, int ns) {
+  const unsigned q = (unsigned)chunks / (unsigned)ns, rest = (unsigned)chunks - q * (unsigned)ns;
+  g.c0 = (int)(q * piece + min((unsigned)piece, rest));   // the first `rest` get one more
+  g.c1 = g.c0 + (int)(q + ((unsigned)piece < rest ? 1u : 0u));
+  g.kind = ns == 1 ? 1 : 2;
+  if (piece == 0 && ns > 1) g.parts = ns;
+}
+
 __device__ __forceinline__ Segment sched_next(const SchedParams& p, const SchedPlan& plan,
                                               SchedWalk& w) {
   Segment g;
-  g.kind = 0;
+  g.kind = g.slot = g.parts = 0;
+  g.stride = 1;
   if (w.at >= w.ub) return g;
+  int piece = 0, item = 0;
+  if (plan.mode == kRounds) {   // the sequence of the item: they differ in their tiles alone
+    const int at = (int)w.at;
+    piece = (int)div_pos(w.at, plan.items);
+    item = at - piece * plan.items;
+    g.slot = (int)div_pos(w.at, p.grid) & 1;
+    g.stride = plan.items;
+    w.at += p.grid;
+    for (w.b = 0;; ++w.b) {
+      const int n = sched_cost(p, w.b).tiles * p.heads;
+      if (item < n) break;
+      item -= n;
+    }
+  }
   for (;;) {
     const SeqRange r = sched_rows(p, w.b), c = sched_cols(p, w.b);
     const SeqCost s = sched_cost(p, r, c);
-    g.last = -1;
-    if (plan.pieces) {
-      const int ns = s.pieces(plan.share), at = (int)(w.at - w.seq_start);   // both at most grid
-      const int item = at / ns, piece = at - item * ns;
+    if (plan.mode != kLine) {
+      int ns = plan.ns;
+      if (plan.mode == kPieces) {
+        ns = s.pieces(plan.share);
+        const int at = (int)(w.at - w.seq_start);   // at most grid, as ns
+        item = at / ns;
+        piece = at - item * ns;
+        w.at = w.ub;
+      }
       g.head = item / s.tiles;
       g.tile = item - g.head * s.tiles;
-      const unsigned chunks = (unsigned)sched_chunks(p, r, c, g.tile), q = chunks / (unsigned)ns;
-      const unsigned rest = chunks - q * (unsigned)ns;   // the first `rest` pieces get one more
-      g.c0 = (int)(q * piece + min((unsigned)piece, rest));
-      g.c1 = g.c0 + (int)(q + ((unsigned)piece < rest ? 1u : 0u));
-      g.kind = ns == 1 ? 1 : 2;
-      if (piece == 0 && ns > 1) g.last = (int)w.at + ns - 1;
-      w.at = w.ub;
+      sched_piece(g, sched_chunks(p, r, c, g.tile), piece, ns);
     } else {
       const long long n = s.before(s.tiles) * p.heads;
       if (w.at >= w.seq_start + n) {   // the sequence is done (or has no rows)
@@ -253,8 +345,11 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, const SchedP
       const long long chunks = sched_chunks(p, r, c, g.tile);
       g.c0 = (int)min(sched_chunks_before(p, x0), chunks);
       g.c1 = (int)(x1 == it.cost ? chunks : min(sched_chunks_before(p, x1), chunks));
-      g.kind = x0 > 0 ? 2 : x1 == it.cost ? 1 : 3;
-      if (g.kind == 3) g.last = (int)div_pos(it.start + it.cost - 1, plan.share);
+      g.kind = x0 == 0 && x1 == it.cost ? 1 : 2;
+      if (x0 == 0 && g.kind == 2) {   // an end or middle is a worker's first, a beginning its last
+        g.slot = 1;
+        g.parts = (int)div_pos(it.start + it.cost - 1, plan.share) - w.worker + 1;
+      }
       w.at = it.start + x1;
     }
     g.b = w.b;
@@ -268,117 +363,125 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, const SchedP
 }
 
 // What the second kernel joins: the item whose first part is worker i's (record
-// i of the workspace), if other workers go on with it (head < 0: none).  Its parts
-// are (i, slot), then (w, 0) up to w = last.
+// i of the workspace), if it has others (head < 0: none).  Part k is at stop
+// i + k * stride: worker stop % grid, slot stop / grid; on the line (stride 1) the
+// first part is in slot `slot`.
 struct SplitItem {
-  int head, tile, slot, last;
-  int row_start, rows, pad0, pad1;
+  int head, tile, slot, parts;
+  int row_start, rows, stride, pad;
 };
+__device__ __forceinline__ SplitItem no_split() { return SplitItem{-1, 0, 0, 0, 0, 0, 0, 0}; }
 __device__ __forceinline__ SplitItem split_of(const Segment& g) {
-  return SplitItem{g.head, g.tile, g.kind == 3 ? 1 : 0, g.last, g.row_start, g.rows, 0, 0};
+  return SplitItem{g.head, g.tile, g.slot, g.parts, g.row_start, g.rows, g.stride, 0};
 }
 __device__ __forceinline__ void store_split(SplitItem* at, const SplitItem& s) {
-  reinterpret_cast<int4*>(at)[0] = make_int4(s.head, s.tile, s.slot, s.last);
-  reinterpret_cast<int4*>(at)[1] = make_int4(s.row_start, s.rows, 0, 0);
+  reinterpret_cast<int4*>(at)[0] = make_int4(s.head, s.tile, s.slot, s.parts);
+  reinterpret_cast<int4*>(at)[1] = make_int4(s.row_start, s.rows, s.stride, 0);
 }
 __device__ __forceinline__ SplitItem load_split(const SplitItem* at) {
   const int4 a = reinterpret_cast<const int4*>(at)[0], b = reinterpret_cast<const int4*>(at)[1];
-  return SplitItem{a.x, a.y, a.z, a.w, b.x, b.y, 0, 0};
+  return SplitItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, 0};
+}
+// Partial slot (2 worker + slot) of part k.
+__device__ __forceinline__ size_t part_slot(const SplitItem& it, int first, int grid, int k) {
+  if (k == 0) return (size_t)first * 2 + it.slot;
+  const int stop = first + k * it.stride;
+  const int round = stop >= grid ? 1 : 0;   // at most two rounds, and none on the line
+  return (size_t)(stop - round * grid) * 2 + round;
 }
 
 // Partial results of attention: per row a maximum (log2 domain) and a sum in
 // part_ml, and 64 unnormalised outputs in part_o; rows of worker w's slot s start
 // at (2 w + s) * tile_rows.
+// Parts stripe, stripe + stripes, ... of one row, by 16 lanes
+// with four dimensions each.  Four parts are loaded at once, before their weights
+// are known.
 struct JoinedRow {
   float m, l;
-  float2 o;   // dimensions 2 lane, 2 lane + 1
+  float4 o;   // dimensions 4 (lane % 16) ..
 };
-// Parts first + stripe, first + stripe + stripes, ... of one row (a warp).  The
-// outputs of eight parts are loaded at once, before the weights are known.
-__device__ __forceinline__ JoinedRow join_row(const SplitItem& it, int first, const float2* part_ml,
-                                              const float* part_o, int tile_rows, int row,
+__device__ __forceinline__ void add_part(JoinedRow& j, float f, float l, const float4& x) {
+  j.l = fmaf(f, l, j.l);
+  j.o.x = fmaf(f, x.x, j.o.x);
+  j.o.y = fmaf(f, x.y, j.o.y);
+  j.o.z = fmaf(f, x.z, j.o.z);
+  j.o.w = fmaf(f, x.w, j.o.w);
+}
+__device__ __forceinline__ JoinedRow join_row(const SplitItem& it, int first, int grid,
+                                              const float2* part_ml, const float* part_o,
+                                              int tile_rows, int row,
                                               int stripe, int stripes) {
-  const int lane = threadIdx.x & 31;
-  JoinedRow j{-INFINITY, 0.f, make_float2(0.f, 0.f)};
-  for (int w0 = first + stripe; w0 <= it.last; w0 += 8 * stripes) {
-    float2 ml[8], x[8];
+  const int lane = threadIdx.x & 15;
+  JoinedRow j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int k0 = stripe; k0 < it.parts; k0 += 4 * stripes) {
+    float2 ml[4];
+    float4 x[4];
     float m = j.m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int w = w0 + i * stripes;
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i * stripes;
       ml[i] = make_float2(-INFINITY, 0.f);
-      x[i] = make_float2(0.f, 0.f);
-      if (w <= it.last) {
-        const size_t part = ((size_t)w * 2 + (w == first ? it.slot : 0)) * tile_rows + row;
+      if (k < it.parts) {
+        const size_t part = part_slot(it, first, grid, k) * tile_rows + row;
         ml[i] = part_ml[part];
-        x[i] = reinterpret_cast<const float2*>(part_o + part * 64)[lane];
+        x[i] = reinterpret_cast<const float4*>(part_o + part * 64)[lane];
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, ml[i].x);
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, ml[i].x);
     if (m == -INFINITY) continue;
     const float a = fast_exp2(j.m - m);
-    j.l *= a, j.o.x *= a, j.o.y *= a;
+    j.l *= a, j.o.x *= a, j.o.y *= a, j.o.z *= a, j.o.w *= a;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (ml[i].x != -INFINITY) {   // otherwise its outputs were not written
-        const float f = fast_exp2(ml[i].x - m);
-        j.l = fmaf(f, ml[i].y, j.l);
-        j.o.x = fmaf(f, x[i].x, j.o.x);
-        j.o.y = fmaf(f, x[i].y, j.o.y);
-      }
+    for (int i = 0; i < 4; ++i)   // without a key of the row its outputs were not written
+      if (ml[i].x != -INFINITY) add_part(j, fast_exp2(ml[i].x - m), ml[i].y, x[i]);
     j.m = m;
   }
   return j;
 }
 
 __device__ __forceinline__ void write_row(const JoinedRow& j, __nv_bfloat16* out, float* lse) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 15;
   const bool empty = j.m == -INFINITY;
   const float inv = empty ? 0.f : 1.0f / j.l;
-  reinterpret_cast<uint32_t*>(out)[lane] = pack_bf16x2(j.o.x * inv, j.o.y * inv);
+  reinterpret_cast<uint2*>(out)[lane] =
+      make_uint2(pack_bf16x2(j.o.x * inv, j.o.y * inv), pack_bf16x2(j.o.z * inv, j.o.w * inv));
   if (lane == 0 && lse != nullptr)
     *lse = empty ? -INFINITY : (j.m + __log2f(j.l)) * 0.6931471805599453f;
 }
 
-// The rows [0, n) of a split item, live where `out_of(row)` is not null, by all
-// warps of a CTA.  Few rows: several warps share a row's parts.
-template <int kWarps, typename OutOf, typename LseOf>
-__device__ __forceinline__ void join_item(const SplitItem& it, int first, const float2* part_ml,
-                                          const float* part_o, int tile_rows, int n, OutOf out_of,
-                                          LseOf lse_of) {
-  __shared__ float2 s_o[kWarps][32];
-  __shared__ float2 s_ml[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int parts = it.last - first + 1;
+// Rows [r0, n) of a split item, live where out_of(row) is not null, by a CTA of
+// kTeams half warps.  Few rows: several half warps share a row's parts.
+template <int kTeams, typename OutOf, typename LseOf>
+__device__ __forceinline__ void join_item(const SplitItem& it, int first, int grid,
+                                          const float2* part_ml, const float* part_o, int tile_rows, int r0, int n,
+                                          OutOf out_of, LseOf lse_of) {
+  __shared__ float4 s_o[kTeams][16];
+  __shared__ float2 s_ml[kTeams];
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
   int stripes = 1;
-  while (stripes < kWarps && n * stripes * 2 <= kWarps && stripes * 8 < parts) stripes *= 2;
-  const int rows_at_once = kWarps / stripes;
-  const int stripe = warp % stripes;
-  for (int r0 = 0; r0 < n; r0 += rows_at_once) {
-    const int r = r0 + warp / stripes;
+  while (stripes < kTeams && (n - r0) * stripes * 2 <= kTeams && stripes * 4 < it.parts) stripes *= 2;
+  const int stripe = team % stripes;
+  for (; r0 < n; r0 += kTeams / stripes) {
+    const int r = r0 + team / stripes;
     __nv_bfloat16* out = r < n ? out_of(r) : nullptr;
-    JoinedRow j{-INFINITY, 0.f, make_float2(0.f, 0.f)};
-    if (out != nullptr) j = join_row(it, first, part_ml, part_o, tile_rows, r, stripe, stripes);
+    JoinedRow j{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (out != nullptr) j = join_row(it, first, grid, part_ml, part_o, tile_rows, r, stripe, stripes);
     if (stripes == 1) {
       if (out != nullptr) write_row(j, out, lse_of(r));
       continue;
     }
     __syncthreads();
-    s_o[warp][lane] = j.o;
-    if (lane == 0) s_ml[warp] = make_float2(j.m, j.l);
+    s_o[team][lane] = j.o;
+    if (lane == 0) s_ml[team] = make_float2(j.m, j.l);
     __syncthreads();
     if (stripe == 0 && out != nullptr) {
       float m = -INFINITY;
-      for (int i = 0; i < stripes; ++i) m = fmaxf(m, s_ml[warp + i].x);
-      JoinedRow t{m, 0.f, make_float2(0.f, 0.f)};
+      for (int i = 0; i < stripes; ++i) m = fmaxf(m, s_ml[team + i].x);
+      JoinedRow t{m, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       if (m != -INFINITY)
-        for (int i = 0; i < stripes; ++i) {
-          const float f = fast_exp2(s_ml[warp + i].x - m);
-          t.l = fmaf(f, s_ml[warp + i].y, t.l);
-          t.o.x = fmaf(f, s_o[warp + i][lane].x, t.o.x);
-          t.o.y = fmaf(f, s_o[warp + i][lane].y, t.o.y);
-        }
+        for (int i = 0; i < stripes; ++i)
+          add_part(t, fast_exp2(s_ml[team + i].x - m), s_ml[team + i].y, s_o[team + i][lane]);
       write_row(t, out, lse_of(r));
     }
   }

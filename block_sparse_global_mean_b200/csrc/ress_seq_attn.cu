@@ -214,7 +214,7 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
     }
   }
   allow_next_kernel();
-  SchedWalk walk{0, 0, 0, 0};
+  SchedWalk walk{0, 0, 0, 0, 0};
   SchedPlan plan;
   if (warp == 2) {
     plan = sched_begin(p.sched, (int)blockIdx.x, &walk);
@@ -281,12 +281,15 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---------------- MMA issue ----------------
+      // The softmax groups wait for this warp's next S, so its path from P(i) to
+      // S(i + 3) is kept short: the stage's copies are awaited before P(i), and PV
+      // and S are issued in one go.
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, false);
       constexpr uint32_t idPV = idesc_bf16_f32(128, 64, true);
-      const uint64_t dq = smem_desc_sw128(smem_addr(sQ), 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(smem_addr(sKV), 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(smem_addr(sKV) + kTileBytes, 16384, 1024);
-      constexpr uint64_t kStageDesc = kStageBytes >> 4, kTileDesc = kTileBytes >> 4;
+      const uint32_t dq = smem_desc_lo(smem_addr(sQ), 16);
+      const uint32_t dk0 = smem_desc_lo(smem_addr(sKV), 16);
+      const uint32_t dv0 = smem_desc_lo(smem_addr(sKV) + kTileBytes, 16384);
+      constexpr uint32_t kStageDesc = kStageBytes >> 4, kTileDesc = kTileBytes >> 4;
       int kc0 = 0, it0 = 0, n_q = 0;
       bool any = false;
       for (int s = 0;; ++s) {
@@ -296,44 +299,50 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
         if (n > 0) {
           bool ok = warp_wait(bar_q, n_q & 1, abortf, p.err, 120);
           any = true;
-          auto issue_s = [&](int i) -> bool {
-            const int kc = kc0 + i / kItemsPerChunk, st = kc % kStages, b = (it0 + i) % kSBufs;
-            if (!warp_wait(bar_kvf + 8 * st, (kc / kStages) & 1, abortf, p.err, 121)) return false;
-            tc_fence_after();
-            const uint64_t a = kPair ? dq + (uint64_t)(i & 1) * kTileDesc : dq;
-            const uint64_t dk = dk0 + (uint64_t)st * kStageDesc;
-            const uint32_t d = tmem + 128u * (uint32_t)b;
-            if (elect_one()) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_ss(d, a + (uint64_t)(kk * 2), dk + (uint64_t)(kk * 2), idS, kk > 0 ? 1u : 0u);
-              mma_commit(bar_s + 8u * (uint32_t)b);
-            }
-            __syncwarp();
-            return true;
+          auto wait_keys = [&](int i) -> bool {
+            const int kc = kc0 + i / kItemsPerChunk;
+            return warp_wait(bar_kvf + 8 * (kc % kStages), (kc / kStages) & 1, abortf, p.err, 121);
           };
-          for (int i = 0; ok && i < n && i < kSBufs; ++i) ok = issue_s(i);
+          auto issue_s = [&](int i, int b) {   // one thread
+            const uint32_t a = kPair ? dq + (uint32_t)(i & 1) * kTileDesc : dq;
+            const uint32_t dk = dk0 + (uint32_t)((kc0 + i / kItemsPerChunk) % kStages) * kStageDesc;
+            const uint32_t d = tmem + 128u * (uint32_t)b;
+            mma_ss_lo<false>(d, a, dk, idS);
+            mma_ss_lo<true>(d, a + 2, dk + 2, idS);
+            mma_ss_lo<true>(d, a + 4, dk + 4, idS);
+            mma_ss_lo<true>(d, a + 6, dk + 6, idS);
+            mma_commit(bar_s + 8u * (uint32_t)b);
+          };
+          for (int i = 0; ok && i < n && i < kSBufs; ++i) {
+            ok = wait_keys(i);
+            tc_fence_after();
+            if (ok && elect_one()) issue_s(i, (it0 + i) % kSBufs);
+            __syncwarp();
+          }
           for (int i = 0; ok && i < n; ++i) {
+            const bool more = i + kSBufs < n;
             const int b = (it0 + i) % kSBufs;
-            if (!warp_wait(bar_p + 8u * (uint32_t)b, ((it0 + i) / kSBufs) & 1, abortf, p.err, 122)) {
+            const int st = (kc0 + i / kItemsPerChunk) % kStages;
+            const uint32_t dv = dv0 + (uint32_t)st * kStageDesc;
+            const uint32_t tP = tmem + 128u * (uint32_t)b;
+            const uint32_t tO = tmem + kColO + 64u * (uint32_t)(i & 1);
+            if ((more && !wait_keys(i + kSBufs)) ||
+                !warp_wait(bar_p + 8u * (uint32_t)b, ((it0 + i) / kSBufs) & 1, abortf, p.err, 122)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const int st = (kc0 + i / kItemsPerChunk) % kStages;
-            const uint64_t dv = dv0 + (uint64_t)st * kStageDesc;
-            const uint32_t tP = tmem + 128u * (uint32_t)b;
-            const uint32_t tO = tmem + kColO + 64u * (uint32_t)(i & 1);
             if (elect_one()) {
+              mma_ts_lo(tO, tP, dv, idPV, i > 1 ? 1u : 0u);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts(tO, tP + kk * 8, dv + (uint64_t)(kk * 128), idPV, (kk > 0 || i > 1) ? 1u : 0u);
-              if (!kPair || (i & 1)) mma_commit(bar_kve + 8 * st);
+              for (int kk = 1; kk < 8; ++kk)
+                mma_ts_lo(tO, tP + kk * 8, dv + kk * 128, idPV, 1u);
               mma_commit(bar_od + 8u * (uint32_t)(i & 1));
+              // S(i + 3) takes the buffer of P(i): the tensor core works in issue order.
+              if (more) issue_s(i + kSBufs, b);
+              if (!kPair || (i & 1)) mma_commit(bar_kve + 8 * st);
             }
             __syncwarp();
-            // S(i + 3) takes the buffer of P(i): the tensor core works in issue order.
-            if (i + kSBufs < n) ok = issue_s(i + kSBufs);
           }
           if (ok && elect_one()) mma_commit(bar_o);
           __syncwarp();
@@ -351,12 +360,12 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
       __syncwarp();
     } else {
       // ---------------- the next item ----------------
-      SplitItem split{-1, 0, 0, 0, 0, 0, 0, 0};
+      SplitItem split = no_split();
       for (int s = 0;; ++s) {
         const Segment& g = ctl->seg[s & 1];
         if (g.kind == 0) break;
         if (threadIdx.x == 64) {
-          if (g.last >= 0) split = split_of(g);
+          if (g.parts > 0) split = split_of(g);
           ctl->seg[(s + 1) & 1] = sched_next(p.sched, plan, walk);
         }
         if (!end_of_item()) break;
@@ -483,7 +492,7 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
           for (int e = 0; e < 16; ++e) {
             const float2 sv = make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1]));
             const float2 x = ffma2(sv, scale2, neg_m2);
-            const float2 pe = ((e & 3) == 3) ? exp2_poly4(x)
+            const float2 pe = ((e & 7) == 7) ? exp2_poly4(x)
                                              : make_float2(fast_exp2(x.x), fast_exp2(x.y));
             if (e & 1) sum_b = fadd2(sum_b, pe);
             else sum_a = fadd2(sum_a, pe);
@@ -538,7 +547,7 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
         tc_fence_after();
         const bool empty = !real || m == -INFINITY;
         const float inv = kind != 1 ? 1.f : empty ? 0.f : 1.0f / l;
-        const size_t part = ((size_t)blockIdx.x * 2 + (kind == 3 ? 1 : 0)) * C::rows +
+        const size_t part = ((size_t)blockIdx.x * 2 + g.slot) * C::rows +
                             (kPair ? par * 128 : 0) + rr;
         if (kind != 1) p.part_ml[part] = empty ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
         else if (live && p.lse != nullptr)
@@ -654,7 +663,7 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
 // Joins the parts of the item that CTA blockIdx.x of the kernel above began
 // and did not end.
 template <bool kPair>
-__global__ void __launch_bounds__(1024) seq_combine_kernel(const __grid_constant__ SeqAttnParams p) {
+__global__ void __launch_bounds__(256) seq_combine_kernel(const __grid_constant__ SeqAttnParams p) {
   constexpr int kRows = kPair ? 256 : 128;
   wait_for_previous_kernel();
   const SplitItem it = load_split(p.split + blockIdx.x);
@@ -665,8 +674,9 @@ __global__ void __launch_bounds__(1024) seq_combine_kernel(const __grid_constant
   const int n = left >= p.sched.tile_rows ? kRows
                 : left > p.tps                ? 128 + (left - p.tps) * p.group
                                               : left * p.group;
-  join_item<32>(
-      it, (int)blockIdx.x, p.part_ml, p.part_o, kRows, n,
+  const int r0 = (int)blockIdx.y * 32;
+  join_item<16>(
+      it, (int)blockIdx.x, p.sched.grid, p.part_ml, p.part_o, kRows, r0, min(n, r0 + 32),
       [&](int r) -> __nv_bfloat16* {
         if ((r & 127) >= p.tps * p.group) return nullptr;
         return p.out + ((size_t)(it.row_start + token_of(r)) * p.heads + head_of(r)) * kHeadDim;
@@ -693,7 +703,8 @@ ress_status launch_seq_typed(const CUtensorMap& tq, const CUtensorMap& tk, const
     return s;
   seq_attn_kernel<kPair, kCache><<<kSms, C::threads, smem, st>>>(tq, tk, tv, p);
   if (ress_status s = record_cuda(cudaGetLastError())) return s;
-  return record_cuda(launch_dependent(seq_combine_kernel<kPair>, dim3(kSms), dim3(1024), st, p));
+  return record_cuda(launch_dependent(seq_combine_kernel<kPair>, dim3(kSms, C::rows / 32),
+                                      dim3(256), st, p));
 }
 
 size_t parts_bytes(bool pair) {
