@@ -120,6 +120,18 @@ ress_status record_cuda(cudaError_t err) {
   return RESS_ERR_CUDA;
 }
 
+ress_status allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (ress_status s = record_cuda(cudaGetDevice(&dev))) return s;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done->load(std::memory_order_relaxed) & bit) return RESS_OK;
+  if (ress_status s = record_cuda(cudaFuncSetAttribute(
+          kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes)))
+    return s;
+  done->fetch_or(bit, std::memory_order_relaxed);
+  return RESS_OK;
+}
+
 DeviceError* device_error_ptr() {
   // One address per device; looked up with that device current.
   static DeviceError* cache[64] = {};

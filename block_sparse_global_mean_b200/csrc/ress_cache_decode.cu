@@ -447,8 +447,9 @@ ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st)
   p.sched.item_cost = kKeys;
   p.sched.min_share = 2 * kKeys;
   p.sched.grid = kWorkers;
-  if (ress_status s = record_cuda(cudaFuncSetAttribute(
-          cache_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)))
+  static std::atomic<uint64_t> allowed{0};
+  if (ress_status s =
+          allow_smem(reinterpret_cast<const void*>(cache_decode_kernel), kSmem, &allowed))
     return s;
   cache_decode_kernel<<<kSms, kWarps * 32, kSmem, st>>>(p);
   if (ress_status s = record_cuda(cudaGetLastError())) return s;

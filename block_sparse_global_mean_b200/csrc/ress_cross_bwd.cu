@@ -705,8 +705,9 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
   // Without rows on one side no item has a chunk, and its maps are not used.
   if (g.nq == 0) tq = tdo = tqg = tdog = tk;
   if (g.nk == 0) tk = tv = tq;
-  if (ress_status e = record_cuda(cudaFuncSetAttribute(
-          cross_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem)))
+  static std::atomic<uint64_t> allowed{0};
+  if (ress_status e =
+          allow_smem(reinterpret_cast<const void*>(cross_bwd_kernel), kSmem, &allowed))
     return e;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ress.h"
 
 namespace ress {
@@ -81,6 +83,10 @@ bool make_rows_map(CUtensorMap* map, const void* base, int heads, int64_t rows,
 // Records `err` as this thread's last CUDA error (for ress_last_cuda_error)
 // and returns RESS_ERR_CUDA, or RESS_OK for cudaSuccess.
 ress_status record_cuda(cudaError_t err);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device, once
+// per device (`done`: a static of the caller, one per kernel).
+ress_status allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>* done);
 
 struct DeviceError;
 // Device address of the error flag on the current device (null on failure).

@@ -698,8 +698,9 @@ ress_status launch_seq_typed(const CUtensorMap& tq, const CUtensorMap& tk, const
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)kSms * 2 * C::rows * kHeadDim);
   p.split = reinterpret_cast<SplitItem*>(p.part_ml + (size_t)kSms * 2 * C::rows);
-  if (ress_status s = record_cuda(cudaFuncSetAttribute(
-          seq_attn_kernel<kPair, kCache>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+  static std::atomic<uint64_t> allowed{0};
+  if (ress_status s =
+          allow_smem(reinterpret_cast<const void*>(seq_attn_kernel<kPair, kCache>), smem, &allowed))
     return s;
   seq_attn_kernel<kPair, kCache><<<kSms, C::threads, smem, st>>>(tq, tk, tv, p);
   if (ress_status s = record_cuda(cudaGetLastError())) return s;

@@ -630,31 +630,43 @@ def _cache_attn_bytes(pages: int, page: int, kv_heads: int, head_dim: int, reque
 def _run_on(device: torch.device, stream: Optional[torch.cuda.Stream], fn, *args) -> int:
     """``_on`` with the stream as the last argument, without a device switch
     where ``device`` is current already."""
+    raw = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
+           else stream.cuda_stream)
     if device.index == torch.cuda.current_device():
-        return fn(*args, _stream_ptr(stream, device))
+        return fn(*args, raw)
     with torch.cuda.device(device):
-        return fn(*args, _stream_ptr(stream, device))
+        return fn(*args, raw)
 
 
-def _new(shape, dtype: torch.dtype, device: torch.device,
+def _new(shape, dtype: torch.dtype, like: torch.Tensor,
          stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A new tensor for a call on ``stream``: allocated on that stream, so that
-    the caching allocator hands its memory to no one before the call is done."""
+    """A new tensor on the device of ``like`` for a call on ``stream``: allocated
+    on that stream, so that the caching allocator hands its memory to no one
+    before the call is done."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(workspace: Optional[torch.Tensor], need: int, device: torch.device,
+def _expect(t: torch.Tensor, shape, dtype: torch.dtype, device: torch.device, name: str) -> int:
+    """``_check_buffer`` and ``_ptr`` in one, for calls that take microseconds."""
+    if (t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_cuda
+            or not t.is_contiguous()):
+        _check_buffer(t, shape, dtype, device, name)
+        return _ptr(t)
+    return t.data_ptr()
+
+
+def _scratch(workspace: Optional[torch.Tensor], need: int, like: torch.Tensor,
              stream: Optional[torch.cuda.Stream]) -> Tuple[Optional[int], int, object]:
     """(pointer, bytes, owner) of a call's workspace."""
     if workspace is not None:
-        _check_workspace(workspace, device)
+        _check_workspace(workspace, like.device)
         return _ptr(workspace), workspace.numel(), workspace
     if need == 0:
         return None, 0, None
-    ws = _new((need,), torch.uint8, device, stream)
+    ws = _new((need,), torch.uint8, like, stream)
     return ws.data_ptr(), need, ws
 
 
@@ -684,35 +696,41 @@ def _check_rows(t: torch.Tensor, name: str, device: torch.device, heads: Optiona
         raise ValueError("tensors must live on a CUDA device")
 
 
-def _seq_arrays(q_offsets, kv_offsets, q_lens, kv_lens, device: torch.device) -> int:
-    """Checks the arrays of a packed batch; returns the number of sequences."""
+def _seq_arrays(q_offsets, kv_offsets, q_lens, kv_lens, device: torch.device):
+    """Checks the arrays of a packed batch; returns the number of sequences and
+    the four pointers."""
     if (q_offsets is None) != (kv_offsets is None):
         raise ValueError("q_offsets and kv_offsets come together")
-    seqs = 1
+    seqs, i32, qo, ko, ql, kl = 1, torch.int32, None, None, None, None
     if q_offsets is not None:
         if q_offsets.dim() != 1 or q_offsets.shape[0] < 2:
             raise ValueError("q_offsets must be [sequences + 1]")
         seqs = q_offsets.shape[0] - 1
-        _check_buffer(q_offsets, (seqs + 1,), torch.int32, device, "q_offsets")
-        _check_buffer(kv_offsets, (seqs + 1,), torch.int32, device, "kv_offsets")
-    for name, t in (("q_lens", q_lens), ("kv_lens", kv_lens)):
-        if t is not None:
-            _check_buffer(t, (seqs,), torch.int32, device, name)
-    return seqs
+        qo = _expect(q_offsets, (seqs + 1,), i32, device, "q_offsets")
+        ko = _expect(kv_offsets, (seqs + 1,), i32, device, "kv_offsets")
+    if q_lens is not None:
+        ql = _expect(q_lens, (seqs,), i32, device, "q_lens")
+    if kv_lens is not None:
+        kl = _expect(kv_lens, (seqs,), i32, device, "kv_lens")
+    return seqs, qo, ko, ql, kl
 
 
 def _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens):
+    """(shape and workspace sizes, pointers of q to kv_lens)."""
     device = q.device
     _check_rows(q, "q", device)
     _check_rows(k, "k", device)
-    if tuple(v.shape) != tuple(k.shape):
+    if v.shape != k.shape:
         raise ValueError(f"v has shape {tuple(v.shape)}, k has {tuple(k.shape)}")
     _check_rows(v, "v", device)
-    if k.shape[2] != q.shape[2]:
-        raise ValueError(f"k has head dim {k.shape[2]}, q has {q.shape[2]}")
-    seqs = _seq_arrays(q_offsets, kv_offsets, q_lens, kv_lens, device)
-    return _cross_shape(q.shape[0], k.shape[0], seqs, q.shape[1], k.shape[1], q.shape[2],
-                        _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v"))
+    nq, h, d = q.shape
+    nk, hk, dk = k.shape
+    if dk != d:
+        raise ValueError(f"k has head dim {dk}, q has {d}")
+    seqs, *arrays = _seq_arrays(q_offsets, kv_offsets, q_lens, kv_lens, device)
+    return (_cross_shape(nq, nk, seqs, h, hk, d, _token_rows(q, "q"), _token_rows(k, "k"),
+                         _token_rows(v, "v")),
+            (q.data_ptr(), k.data_ptr(), v.data_ptr()), arrays)
 
 
 def ress_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -731,22 +749,29 @@ def ress_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     each that are not padding.  Token rows of q, k and v may be slices of
     wider rows.  Rows of no sequence are left as they were (undefined in a
     tensor that this call allocates).  See include/ress.h."""
-    sh, need, _ = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
+    (sh, need, _), qkv, arrays = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
     device, (nq, h, _) = q.device, q.shape
-    if out is None:
-        out = _new(q.shape, q.dtype, device, stream)
-    else:
-        _check_buffer(out, q.shape, q.dtype, device, "out")
-    if lse is not None:
-        _check_buffer(lse, (h, nq), torch.float32, device, "lse")
-    elif want_lse:
-        lse = _new((h, nq), torch.float32, device, stream)
-    ws, size, owner = _scratch(workspace, need, device, stream)
-    status = _run_on(device, stream, lib.ress_cross_attn, sh, q.data_ptr(), k.data_ptr(),
-                     v.data_ptr(), _ptr(q_offsets), _ptr(kv_offsets), _ptr(q_lens), _ptr(kv_lens),
-                     _ptr(out), _ptr(lse), ws, size)
-    _check(status, "ress_cross_attn")
+    out, out_ptr, lse, lse_ptr = _attn_outputs(q, out, lse, want_lse, stream)
+    ws, size, owner = _scratch(workspace, need, q, stream)
+    _check(_run_on(device, stream, lib.ress_cross_attn, sh, *qkv, *arrays, out_ptr, lse_ptr, ws,
+                   size), "ress_cross_attn")
     return out, lse
+
+
+def _attn_outputs(q, out, lse, want_lse, stream):
+    """The output tensors of an attention call over q and their pointers."""
+    nq, h, _ = q.shape
+    if out is None:
+        out = _new(q.shape, q.dtype, q, stream)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _expect(out, q.shape, q.dtype, q.device, "out")
+    if lse is not None:
+        return out, out_ptr, lse, _expect(lse, (h, nq), torch.float32, q.device, "lse")
+    if not want_lse:
+        return out, out_ptr, None, None
+    lse = _new((h, nq), torch.float32, q, stream)
+    return out, out_ptr, lse, lse.data_ptr()
 
 
 def ress_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -762,24 +787,22 @@ def ress_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
                         ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients of ress_cross_attn: returns (dq, dk, dv) in the shapes of q,
     k and v, from what the forward call returned and dout [nq, H, 64]."""
-    sh, _, need = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
+    (sh, _, need), qkv, arrays = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
     device, (nq, h, _) = q.device, q.shape
-    _check_buffer(out, q.shape, q.dtype, device, "out")
-    _check_buffer(dout, q.shape, q.dtype, device, "dout")
-    _check_buffer(lse, (h, nq), torch.float32, device, "lse")
-    grads = []
+    saved = (_expect(out, q.shape, q.dtype, device, "out"),
+             _expect(lse, (h, nq), torch.float32, device, "lse"),
+             _expect(dout, q.shape, q.dtype, device, "dout"))
+    grads, ptrs = [], []
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
         if t is None:
-            t = _new(like.shape, like.dtype, device, stream)
+            t = _new(like.shape, like.dtype, q, stream)
+            ptrs.append(t.data_ptr())
         else:
-            _check_buffer(t, like.shape, like.dtype, device, name)
+            ptrs.append(_expect(t, like.shape, like.dtype, device, name))
         grads.append(t)
-    ws, size, owner = _scratch(workspace, need, device, stream)
-    status = _run_on(device, stream, lib.ress_cross_attn_bwd, sh, q.data_ptr(), k.data_ptr(),
-                     v.data_ptr(), _ptr(out), _ptr(lse), _ptr(dout), _ptr(q_offsets),
-                     _ptr(kv_offsets), _ptr(q_lens), _ptr(kv_lens), _ptr(grads[0]),
-                     _ptr(grads[1]), _ptr(grads[2]), ws, size)
-    _check(status, "ress_cross_attn_bwd")
+    ws, size, owner = _scratch(workspace, need, q, stream)
+    _check(_run_on(device, stream, lib.ress_cross_attn_bwd, sh, *qkv, *saved, *arrays, *ptrs, ws,
+                   size), "ress_cross_attn_bwd")
     return grads[0], grads[1], grads[2]
 
 
@@ -801,16 +824,19 @@ def make_cache(pages: int, kv_heads: int, page: int, device="cuda") -> ress_cach
                                 for _ in range(2)))
 
 
-def _check_cache(cache: ress_cache, device: torch.device) -> Tuple[int, int, int, int]:
-    """(pages, page, kv_heads, head_dim) of a cache whose parts fit together."""
-    if cache.k.dim() != 4:
+def _check_cache(cache: ress_cache, device: torch.device):
+    """(pages, page, kv_heads, head_dim) of a cache whose parts fit together, and
+    the pointers of its parts."""
+    k, v, k_scale, v_scale = cache
+    if k.dim() != 4:
         raise ValueError("cache.k must be [pages, heads, page, d]")
-    pages, heads, page, d = cache.k.shape
-    _check_buffer(cache.k, cache.k.shape, torch.float8_e4m3fn, device, "cache.k")
-    _check_buffer(cache.v, cache.k.shape, torch.float8_e4m3fn, device, "cache.v")
-    _check_buffer(cache.k_scale, (pages, heads), torch.float32, device, "cache.k_scale")
-    _check_buffer(cache.v_scale, (pages, heads), torch.float32, device, "cache.v_scale")
-    return pages, page, heads, d
+    shape = k.shape
+    pages, heads, page, d = shape
+    return (pages, page, heads, d), (
+        _expect(k, shape, torch.float8_e4m3fn, device, "cache.k"),
+        _expect(v, shape, torch.float8_e4m3fn, device, "cache.v"),
+        _expect(k_scale, (pages, heads), torch.float32, device, "cache.k_scale"),
+        _expect(v_scale, (pages, heads), torch.float32, device, "cache.v_scale"))
 
 
 def ress_cache_plan(added: torch.Tensor, lengths: torch.Tensor, table: torch.Tensor,
@@ -824,31 +850,32 @@ def ress_cache_plan(added: torch.Tensor, lengths: torch.Tensor, table: torch.Ten
     """Block tables and slot maps for ``added`` [R] tokens behind ``lengths``
     [R] cached ones: extends ``table`` [R, max_pages] in place from
     ``free_pages[cursor:]`` and returns (offsets [R + 1], slots [tokens],
-    new_lengths [R], new_cursor [1]), all int32.  ``tokens`` is the length of
-    the slot map (at least the sum of ``added``); ``pages`` bounds the page ids
+    new_lengths [R], new_cursor [1]), all int32 (parts of one allocation unless
+    any is passed in).  ``tokens`` is the length of the slot map (at least the sum of ``added``); ``pages`` bounds the page ids
     (default: the largest pool).  See include/ress.h."""
-    device = added.device
+    device, i32 = added.device, torch.int32
     if added.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("added must be [R], table [R, max_pages], free_pages [n]")
-    r, width = table.shape
-    for name, t, shape in (("added", added, (r,)), ("lengths", lengths, (r,)),
-                           ("table", table, (r, width)),
-                           ("free_pages", free_pages, free_pages.shape), ("cursor", cursor, (1,))):
-        _check_buffer(t, shape, torch.int32, device, name)
-    made = []
-    for name, t, n in (("offsets", offsets, r + 1), ("slots", slots, int(tokens)),
-                       ("new_lengths", new_lengths, r), ("new_cursor", new_cursor, 1)):
-        if t is None:
-            t = _new((n,), torch.int32, device, stream)
-        else:
-            _check_buffer(t, (n,), torch.int32, device, name)
-        made.append(t)
+    (r, width), tokens = table.shape, int(tokens)
+    ins = (_expect(added, (r,), i32, device, "added"),
+           _expect(lengths, (r,), i32, device, "lengths"),
+           _expect(table, (r, width), i32, device, "table"),
+           _expect(free_pages, free_pages.shape, i32, device, "free_pages"),
+           free_pages.shape[0], _expect(cursor, (1,), i32, device, "cursor"))
+    sizes = (r + 1, tokens, r, 1)
+    if tokens >= 0 and offsets is slots is new_lengths is new_cursor is None:
+        made = _new((sum(sizes),), i32, added, stream).split_with_sizes(sizes)
+        ptrs = [t.data_ptr() for t in made]
+    else:
+        made, ptrs = [], []
+        for name, t, n in zip(("offsets", "slots", "new_lengths", "new_cursor"),
+                              (offsets, slots, new_lengths, new_cursor), sizes):
+            made.append(_new((n,), i32, added, stream) if t is None else t)
+            ptrs.append(_expect(made[-1], (n,), i32, device, name))
     limit = (2 ** 31 - 1) // max(int(page), 1) if pages is None else pages
-    status = _run_on(device, stream, lib.ress_cache_plan,
-                     _cache_shape(limit, int(page), 1, 64, r, width), _ptr(added), _ptr(lengths),
-                     _ptr(table), _ptr(free_pages), free_pages.shape[0], _ptr(cursor),
-                     int(tokens), _ptr(made[0]), _ptr(made[1]), _ptr(made[2]), _ptr(made[3]))
-    _check(status, "ress_cache_plan")
+    _check(_run_on(device, stream, lib.ress_cache_plan,
+                   _cache_shape(limit, int(page), 1, 64, r, width), *ins, tokens, *ptrs),
+           "ress_cache_plan")
     return made[0], made[1], made[2], made[3]
 
 
@@ -858,19 +885,18 @@ def ress_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cac
     slices of wider ones) into the cells ``slots`` [tokens] int32 of ``cache``,
     in place; negative slots skip their token.  See include/ress.h."""
     device = k.device
-    pages, page, heads, d = _check_cache(cache, device)
+    (pages, page, heads, d), parts = _check_cache(cache, device)
     _check_rows(k, "k", device, heads, (torch.bfloat16, torch.float32))
-    if tuple(v.shape) != tuple(k.shape) or k.shape[2] != d:
+    if v.shape != k.shape or k.shape[2] != d:
         raise ValueError(f"k and v must be [tokens, {heads}, {d}], got {tuple(k.shape)} and "
                          f"{tuple(v.shape)}")
     _check_rows(v, "v", device, heads, (k.dtype,))
-    _check_buffer(slots, (k.shape[0],), torch.int32, device, "slots")
-    status = _run_on(device, stream, lib.ress_cache_append,
-                     _cache_shape(pages, page, heads, d, 1, 1), k.data_ptr(), v.data_ptr(),
-                     RESS_F32 if k.dtype == torch.float32 else RESS_BF16, _token_rows(k, "k"),
-                     _token_rows(v, "v"), _ptr(slots), k.shape[0], _ptr(cache.k), _ptr(cache.v),
-                     _ptr(cache.k_scale), _ptr(cache.v_scale))
-    _check(status, "ress_cache_append")
+    n = k.shape[0]
+    _check(_run_on(device, stream, lib.ress_cache_append,
+                   _cache_shape(pages, page, heads, d, 1, 1), k.data_ptr(), v.data_ptr(),
+                   RESS_F32 if k.dtype is torch.float32 else RESS_BF16, _token_rows(k, "k"),
+                   _token_rows(v, "v"), _expect(slots, (n,), torch.int32, device, "slots"), n,
+                   *parts), "ress_cache_append")
 
 
 def ress_cache_attn(q: torch.Tensor, cache: ress_cache, table: torch.Tensor,
@@ -887,34 +913,25 @@ def ress_cache_attn(q: torch.Tensor, cache: ress_cache, table: torch.Tensor,
     max_pages] names their pages.  ``step`` 0: every query sees all of its
     request; 1: causal; n: groups of n tokens see themselves and the earlier
     groups.  See include/ress.h."""
-    device = q.device
-    pages, page, heads, d = _check_cache(cache, device)
+    device, i32 = q.device, torch.int32
+    (pages, page, heads, d), parts = _check_cache(cache, device)
     _check_rows(q, "q", device)
-    if q.shape[2] != d:
-        raise ValueError(f"q has head dim {q.shape[2]}, the cache {d}")
+    n, h, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q has head dim {dq}, the cache {d}")
     if table.dim() != 2:
         raise ValueError("table must be [requests, max_pages]")
     r, width = table.shape
-    _check_buffer(table, (r, width), torch.int32, device, "table")
-    _check_buffer(lengths, (r,), torch.int32, device, "lengths")
-    _check_buffer(offsets, (r + 1,), torch.int32, device, "offsets")
-    n, h, _ = q.shape
-    if out is None:
-        out = _new(q.shape, q.dtype, device, stream)
-    else:
-        _check_buffer(out, q.shape, q.dtype, device, "out")
-    if lse is not None:
-        _check_buffer(lse, (h, n), torch.float32, device, "lse")
-    elif want_lse:
-        lse = _new((h, n), torch.float32, device, stream)
+    arrays = (_expect(table, (r, width), i32, device, "table"),
+              _expect(lengths, (r,), i32, device, "lengths"),
+              _expect(offsets, (r + 1,), i32, device, "offsets"))
+    out, out_ptr, lse, lse_ptr = _attn_outputs(q, out, lse, want_lse, stream)
     ws, size, owner = _scratch(workspace, _cache_attn_bytes(pages, page, heads, d, r, width, h, n),
-                               device, stream)
-    status = _run_on(device, stream, lib.ress_cache_attn,
-                     _cache_shape(pages, page, heads, d, r, width), h, n, q.data_ptr(),
-                     _token_rows(q, "q"), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale),
-                     _ptr(cache.v_scale), _ptr(table), _ptr(lengths), _ptr(offsets), int(step),
-                     _ptr(out), _ptr(lse), ws, size)
-    _check(status, "ress_cache_attn")
+                               q, stream)
+    _check(_run_on(device, stream, lib.ress_cache_attn,
+                   _cache_shape(pages, page, heads, d, r, width), h, n, q.data_ptr(),
+                   _token_rows(q, "q"), *parts, *arrays, int(step), out_ptr, lse_ptr, ws, size),
+           "ress_cache_attn")
     return out, lse
 
 

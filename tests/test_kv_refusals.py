@@ -190,7 +190,7 @@ def test_binding_refuses_mismatched_tensors(ress):
         """A host tensor that says it is on a device, to reach the later checks."""
         is_cuda = True
 
-    q, k = q.as_subclass(Fake), k.as_subclass(Fake)
+    q, k, off = (t.as_subclass(Fake) for t in (q, k, off))
     with pytest.raises(ValueError, match="v has shape"):
         ress.ress_cross_attn(q, k, k[:19])
     with pytest.raises(ValueError, match="come together"):
@@ -204,12 +204,13 @@ def test_binding_refuses_mismatched_tensors(ress):
     with pytest.raises(ValueError, match="out must have shape"):
         ress.ress_cross_attn(q, k, k, out=k)
     with pytest.raises(ValueError, match="dout must have shape"):
-        ress.ress_cross_attn_bwd(q, k, k, q, torch.zeros(4, 10), k)
+        ress.ress_cross_attn_bwd(q, k, k, q, torch.zeros(4, 10).as_subclass(Fake), k)
     with pytest.raises(ValueError, match="lse must have shape"):
-        ress.ress_cross_attn_bwd(q, k, k, q, torch.zeros(10, 4), q)
+        ress.ress_cross_attn_bwd(q, k, k, q, torch.zeros(10, 4).as_subclass(Fake), q)
 
-    cache = ress.make_cache(4, 2, 64, device="cpu")
-    slots = torch.zeros(20, dtype=i32)
+    cache = ress.ress_cache(*(t.as_subclass(Fake)
+                              for t in ress.make_cache(4, 2, 64, device="cpu")))
+    slots = torch.zeros(20, dtype=i32).as_subclass(Fake)
     with pytest.raises(ValueError, match="heads"):
         ress.ress_cache_append(q, q, slots, cache)
     with pytest.raises(ValueError, match="slots must have shape"):
@@ -222,13 +223,14 @@ def test_binding_refuses_mismatched_tensors(ress):
         ress.ress_cache_append(k, k, slots, cache._replace(v=cache.v[:3]))
     with pytest.raises(TypeError, match="cache.k must be"):
         ress.ress_cache_append(k, k, slots, cache._replace(k=cache.k.to(bf)))
+    table = torch.zeros(2, 3, dtype=i32).as_subclass(Fake)
     with pytest.raises(ValueError, match="offsets must have shape"):
-        ress.ress_cache_attn(q, cache, torch.zeros(2, 3, dtype=i32), torch.zeros(2, dtype=i32),
-                             torch.zeros(2, dtype=i32))
+        ress.ress_cache_attn(q, cache, table, off[:2], off[:2])
     with pytest.raises(ValueError, match="table must be"):
         ress.ress_cache_attn(q, cache, torch.zeros(2, dtype=i32), torch.zeros(2, dtype=i32),
                              torch.zeros(3, dtype=i32))
+    table = torch.zeros(3, 4, dtype=i32).as_subclass(Fake)
     with pytest.raises(ValueError, match="lengths must have shape"):
-        ress.ress_cache_plan(off, off[:2], torch.zeros(3, 4, dtype=i32), off, off[:1], 64, 9)
+        ress.ress_cache_plan(off, off[:2], table, off, off[:1], 64, 9)
     with pytest.raises(ValueError, match="cursor must have shape"):
-        ress.ress_cache_plan(off, off, torch.zeros(3, 4, dtype=i32), off, off, 64, 9)
+        ress.ress_cache_plan(off, off, table, off, off, 64, 9)
