@@ -209,6 +209,7 @@ ress_status ress_cache_append(const ress_cache_shape* shape, const void* k, cons
   if (ress_status s = check_pool(shape, true)) return s;
   if (dtype != RESS_BF16 && dtype != RESS_F32) return RESS_ERR_INVALID_ARG;
   if (tokens < 0) return RESS_ERR_INVALID_ARG;
+  if ((int64_t)tokens > kMaxTokens / 2) return RESS_ERR_UNSUPPORTED;   // bounds the grid
   const int unit = dtype == RESS_F32 ? 4 : 8;
   const int64_t width = (int64_t)shape->kv_heads * kHeadDim;
   const long long ks = row_stride(k_stride, width, unit), vs = row_stride(v_stride, width, unit);

@@ -173,7 +173,7 @@ struct AppendParams {
   const int32_t* slots;
   uint8_t* cache[2];           // [pages][kv_heads][page][64] codes
   float* scale[2];             // [pages][kv_heads]
-  int tokens, kv_heads, page, page_log2, pages;
+  int tokens, kv_heads, page, pages;
 };
 
 // Exponent e of the smallest power of two with amax <= 448 * 2^e, at least
@@ -197,116 +197,158 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// Eight consecutive values of a token row.
+// Eight consecutive values of a token row, as they stand in memory and in float32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&v)[8]);
+struct Eight;
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* src, float (&v)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+struct Eight<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* src) {
+    w = __ldg(reinterpret_cast<const uint4*>(src));
   }
-}
+  __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
 template <>
-__device__ __forceinline__ void load8<float>(const float* src, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(src));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(src) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* src) {
+    a = __ldg(reinterpret_cast<const float4*>(src));
+    b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
 
-// One warp per (window of tokens, head, tensor): it finds the runs that start
-// in its window (a run: consecutive slots within one page) and for each takes
-// the largest magnitude, the page's scale, then writes the codes.
-template <typename T, int kWindow>
-__global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int which = (int)(w & 1);
-  const int head = (int)((w >> 1) % p.kv_heads);
-  const long long t0 = (w >> 1) / p.kv_heads * kWindow;
-  if (t0 >= p.tokens) return;
-  const int mask = p.page - 1;
-  const int t = (int)t0 + lane;
-  bool starts = false;
-  if (lane < kWindow && t < p.tokens) {
-    const int s = p.slots[t];
-    if (s >= 0) {
-      const int prev = t > 0 ? p.slots[t - 1] : -1;
-      starts = (s & mask) == 0 || prev < 0 || prev + 1 != s;
+// A CTA per (window of `window` tokens, head, tensor), a thread per token of a
+// page.  It finds the runs that start in its window (a run: consecutive slots
+// within one page) from two bit masks, and each run passes through registers
+// once: every warp loads 32 of its tokens, eight loads per lane in flight; the
+// largest magnitude gives the page's scale; the codes go out 256 bytes per
+// warp and store.
+template <typename T, int kPage>
+__global__ void __launch_bounds__(kPage) cache_append_kernel(const AppendParams p, int window) {
+  constexpr int kWarps = kPage / 32;
+  __shared__ uint32_t s_cont[2 * kWarps + 1];   // token goes on with the run of the one before
+  __shared__ uint32_t s_start[kWarps];          // token of the window that starts a run
+  __shared__ float s_amax[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int which = (int)(blockIdx.x & 1u);
+  const int head = (int)((blockIdx.x >> 1) % (unsigned)p.kv_heads);
+  const long long t0 = (long long)((blockIdx.x >> 1) / (unsigned)p.kv_heads) * window;
+  constexpr int mask = kPage - 1;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const long long pos = t0 + u * kPage + threadIdx.x;
+    bool cont = false, start = false;
+    if (pos < p.tokens) {
+      const int s = __ldg(p.slots + pos);
+      const int prev = pos > 0 ? __ldg(p.slots + pos - 1) : -1;
+      cont = s >= 0 && prev >= 0 && prev + 1 == s && (s & mask) != 0;
+      start = u == 0 && s >= 0 && !cont && (int)threadIdx.x < window;
+    }
+    const unsigned c = __ballot_sync(0xffffffffu, cont), b = __ballot_sync(0xffffffffu, start);
+    if (lane == 0) {
+      s_cont[u * kWarps + warp] = c;
+      if (u == 0) s_start[warp] = b;
     }
   }
-  unsigned todo = __ballot_sync(0xffffffffu, starts);
-  const T* x = static_cast<const T*>(p.x[which]) + (size_t)head * 64;
-  const long long stride = p.stride[which];
-  const int sub = lane >> 3, col = (lane & 7) * 8;   // four rows of eight 8-value pieces
-  while (todo) {
-    const int first = (int)t0 + __ffs((int)todo) - 1;
-    todo &= todo - 1u;
-    const int slot = p.slots[first];
-    const int page = slot >> p.page_log2, c = slot & mask;
-    if (page >= p.pages) {
-      if (lane == 0) raise_device_error(p.err, RESS_ERR_BAD_INDEX, 104);
-      continue;
-    }
-    // Tokens of the run: those whose slots go on counting, up to the page's end.
-    const int most = min(p.page - c, p.tokens - first);
-    int n = 0;
-    for (int i0 = 0; i0 < most; i0 += 32) {
-      const int i = i0 + lane;
-      const unsigned on = __ballot_sync(0xffffffffu, i < most && p.slots[first + i] == slot + i);
-      if (on != 0xffffffffu) {
-        n = i0 + __ffs((int)~on) - 1;
-        break;
+  if (threadIdx.x == 0) s_cont[2 * kWarps] = 0u;
+  __syncthreads();
+  // Choices, not indexes: an indexed parameter would be copied to local memory.
+  const T* x = static_cast<const T*>(which ? p.x[1] : p.x[0]) + (size_t)head * 64;
+  const long long stride = which ? p.stride[1] : p.stride[0];
+  uint8_t* const cache = which ? p.cache[1] : p.cache[0];
+  float* const scales = which ? p.scale[1] : p.scale[0];
+  const int col = (lane & 7) * 8;
+  const int row0 = warp * 32 + (lane >> 3);   // of the run; then every fourth
+  for (int word = 0; word < kWarps; ++word) {
+    for (uint32_t todo = s_start[word]; todo != 0; todo &= todo - 1u) {
+      const int bit = word * 32 + __ffs((int)todo) - 1;
+      const long long first = t0 + bit;
+      const int slot = __ldg(p.slots + first);
+      const int page = slot / kPage, c = slot & mask;
+      if (page >= p.pages) {
+        if (threadIdx.x == 0) raise_device_error(p.err, RESS_ERR_BAD_INDEX, 104);
+        continue;
       }
-      n = i0 + 32;
-    }
-    float amax = 0.f;
-    for (int i = sub; i < n; i += 4) {
-      float v[8];
-      load8(x + (first + i) * stride + col, v);
+      int n = 1;
+      for (int i = bit + 1;;) {   // the tokens that go on with it (never past the page's end)
+        const uint32_t off = ~(s_cont[i >> 5] >> (i & 31));
+        const int room = 32 - (i & 31), ones = off == 0u ? 32 : __ffs((int)off) - 1;
+        n += min(ones, room);
+        if (ones < room || (i = (i | 31) + 1) >= 2 * kPage) break;
+      }
+      Eight<T> v[8];
+      float* scale_at = scales + (size_t)page * p.kv_heads + head;
+      const float old = c > 0 ? *scale_at : 0.f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(v[u]));
-    }
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float* scale_at = p.scale[which] + (size_t)page * p.kv_heads + head;
-    const float old = c > 0 ? *scale_at : 0.f;
-    const float now = fmaxf(pow2(scale_exponent(amax)), old);
-    const float inv = 1.0f / now;   // exact: a power of two
-    uint8_t* dst = p.cache[which] + (((size_t)page * p.kv_heads + head) << p.page_log2) * 64;
-    for (int i = sub; i < n; i += 4) {
-      float v[8];
-      load8(x + (first + i) * stride + col, v);
-      uint2 o;
-      o.x = e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16;
-      o.y = e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16;
-      *reinterpret_cast<uint2*>(dst + (size_t)(c + i) * 64 + col) = o;
-    }
-    if (now != old) {
-      __syncwarp();
-      if (lane == 0) *scale_at = now;
-      const float ratio = old * inv;
-      for (int i = lane; i < c * 16; i += 32) {   // older codes, four at a time
-        uint32_t* at = reinterpret_cast<uint32_t*>(dst) + i;
-        const uint32_t codes = *at;
-        const float2 a = from_e4m3x2(codes & 0xffffu), b = from_e4m3x2(codes >> 16);
-        *at = e4m3x2(a.x * ratio, a.y * ratio) | e4m3x2(b.x * ratio, b.y * ratio) << 16;
+      for (int k = 0; k < 8; ++k) {
+        if (row0 + 4 * k < n) v[k].load(x + (first + row0 + 4 * k) * stride + col);
+        else v[k].zero();
       }
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float f[8];
+        v[k].get(f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(f[u]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (lane == 0) s_amax[warp] = amax;
+      __syncthreads();   // (and every thread has read the old scale)
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_amax[w]);
+      const float now = fmaxf(pow2(scale_exponent(amax)), old);
+      const float inv = 1.0f / now;   // exact: a power of two
+      uint8_t* dst = cache + ((size_t)page * p.kv_heads + head) * kPage * 64;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (row0 + 4 * k < n) {
+          float f[8];
+          v[k].get(f);
+          uint2 o;
+          o.x = e4m3x2(f[0] * inv, f[1] * inv) | e4m3x2(f[2] * inv, f[3] * inv) << 16;
+          o.y = e4m3x2(f[4] * inv, f[5] * inv) | e4m3x2(f[6] * inv, f[7] * inv) << 16;
+          *reinterpret_cast<uint2*>(dst + (c + row0 + 4 * k) * 64 + col) = o;
+        }
+      }
+      if (now != old) {
+        if (threadIdx.x == 0) *scale_at = now;
+        const float ratio = old * inv;
+        for (int i = threadIdx.x; i < c * 16; i += kPage) {   // older codes, four at a time
+          uint32_t* at = reinterpret_cast<uint32_t*>(dst) + i;
+          const uint32_t codes = *at;
+          const float2 a = from_e4m3x2(codes & 0xffffu), b = from_e4m3x2(codes >> 16);
+          *at = e4m3x2(a.x * ratio, a.y * ratio) | e4m3x2(b.x * ratio, b.y * ratio) << 16;
+        }
+      }
+      __syncthreads();   // s_amax is free again
     }
   }
 }
 
 template <typename T>
 void launch_append_typed(const AppendParams& p, cudaStream_t st) {
-  // Short calls (a few tokens each in a page of its own) take a warp per
-  // token, long ones (whole pages) a warp per 32 tokens.
-  const int window = p.tokens <= 1024 ? 1 : 32;
-  const long long warps = ((long long)p.tokens + window - 1) / window * p.kv_heads * 2;
-  const unsigned blocks = (unsigned)((warps + 7) / 8);
-  if (window == 1) cache_append_kernel<T, 1><<<blocks, 256, 0, st>>>(p);
-  else cache_append_kernel<T, 32><<<blocks, 256, 0, st>>>(p);
+  // Runs that start in one window are written one after another.  Whole views
+  // start one run per page of tokens, so a window is a page; short calls (a few
+  // tokens each for many requests) start one per token or few.
+  const int window = p.tokens <= 1024 ? 1 : p.tokens <= 4096 ? 8 : p.page;
+  const unsigned blocks = (unsigned)(((long long)p.tokens + window - 1) / window * p.kv_heads * 2);
+  if (p.page == 64) cache_append_kernel<T, 64><<<blocks, 64, 0, st>>>(p, window);
+  else cache_append_kernel<T, 128><<<blocks, 128, 0, st>>>(p, window);
 }
 
 }  // namespace
@@ -366,7 +408,6 @@ ress_status launch_cache_append(const ress_cache_shape& s, const void* k, const 
   p.tokens = tokens;
   p.kv_heads = s.kv_heads;
   p.page = s.page;
-  p.page_log2 = s.page == 64 ? 6 : 7;
   p.pages = s.pages;
   if (f32) launch_append_typed<float>(p, st);
   else launch_append_typed<__nv_bfloat16>(p, st);

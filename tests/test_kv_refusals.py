@@ -152,6 +152,7 @@ def test_cache_calls_refuse_arguments(ress):
     for i in range(7):
         assert append({i: None}) == bad and append({i: FAKE + 2}) == bad, i
     assert append(dtype=2) == bad and append(tokens=-1) == bad
+    assert append(tokens=2 ** 29 + 1) == ress.RESS_ERR_UNSUPPORTED
     assert append(ks=64) == bad and append(vs=2 * 64 + 4) == bad
     assert append({i: None for i in range(7)}, tokens=0) == ress.RESS_OK
 
