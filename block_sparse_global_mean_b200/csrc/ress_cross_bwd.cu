@@ -445,7 +445,7 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
                                                 __uint_as_float(r[q][4 * e + 3])),
                                     scale2, make_float2(nl4.z, nl4.w));
             const float2 p0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
-            const float2 p1 = (e & 1) ? exp2_poly4(x1) : make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
+            const float2 p1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
             r[q][4 * e] = __float_as_uint(p0.x);
             r[q][4 * e + 1] = __float_as_uint(p0.y);
             r[q][4 * e + 2] = __float_as_uint(p1.x);

@@ -762,7 +762,8 @@ def _attn_outputs(q, out, lse, want_lse, stream):
     """The output tensors of an attention call over q and their pointers."""
     nq, h, _ = q.shape
     if out is None:
-        out = _new(q.shape, q.dtype, q, stream)
+        out = (torch.empty_like(q) if stream is None and q.is_contiguous()
+               else _new(q.shape, q.dtype, q, stream))
         out_ptr = out.data_ptr()
     else:
         out_ptr = _expect(out, q.shape, q.dtype, q.device, "out")
