@@ -19,9 +19,16 @@
 //   P = exp2(X log2(e) / 8 - lse log2(e)),  dS = P (Y - delta)
 //   key walk: dV += P B2, dK += dS B1;  query walk: dQ += dS B1.
 //
-// TMEM (512 columns): X of the two softmax groups (2 x 128; P and dS as bf16
-// over it once it is in registers), one Y (128, free again when it has been
-// read), two accumulators (64 each).
+// P and dS enter as bf16.  A row of dS sums to zero over its keys, so what keys
+// have in common (their mean) cancels in dQ, but roundings of dS do not sum to
+// zero: with keys whose mean is twice their spread a single bf16 dS left 0.41 %
+// in dQ against 0.17 % of the output's own rounding.  The query walk therefore
+// multiplies dS as two bf16 numbers, its rounding and the rest (16 bits of it).
+// dK and dV have no such sum; they are off by 0.23 %.
+//
+// TMEM (512 columns): X of the two softmax groups (2 x 128; P, or the rest of dS,
+// and dS as bf16 over it once it is in registers), one Y (128, free again when it
+// has been read), two accumulators (64 each).
 //
 // Warp roles: 0 TMA, 1 TMEM and MMA issue, 2 the next item, 3 (key walk) lse and
 // delta of the chunk's rows, 4-11 two groups of four warps that take the even
@@ -115,6 +122,12 @@ __global__ void __launch_bounds__(256)
     nl[(size_t)h * nq + row] = l == -INFINITY ? l : -l * kLog2e;
     nd[(size_t)h * nq + row] = -d;
   }
+}
+
+// x less its bf16 rounding (the pair `hi`), as bf16.
+__device__ __forceinline__ uint32_t rest_bf16x2(float2 x, uint32_t hi) {
+  const float2 r = fadd2(x, make_float2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xffff0000u)));
+  return pack_bf16x2(r.x, r.y);
 }
 
 template <bool kDQ>
@@ -317,6 +330,11 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
               for (int kk = 0; kk < 8; ++kk)
                 mma_ts(tmem + kColA2, tP + 64 + kk * 8, t1 + (uint64_t)(kk * 128), idA,
                        (kk > 0 || i > 0) ? 1u : 0u);
+              if (kDQ) {
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                  mma_ts(tmem + kColA2, tP + kk * 8, t1 + (uint64_t)(kk * 128), idA, 1u);
+              }
               mma_commit(bar_be + 8 * st);
             }
             __syncwarp();
@@ -502,14 +520,17 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
             const float2 d1 = fmul2(p1, fadd2(make_float2(__uint_as_float(y[4 * e + 2]),
                                                           __uint_as_float(y[4 * e + 3])),
                                               make_float2(nd4.z, nd4.w)));
-            if (!kDQ) {
+            dk[2 * e] = pack_bf16x2(d0.x, d0.y);
+            dk[2 * e + 1] = pack_bf16x2(d1.x, d1.y);
+            if (kDQ) {   // what the rounding leaves
+              pk[2 * e] = rest_bf16x2(d0, dk[2 * e]);
+              pk[2 * e + 1] = rest_bf16x2(d1, dk[2 * e + 1]);
+            } else {
               pk[2 * e] = pack_bf16x2(p0.x, p0.y);
               pk[2 * e + 1] = pack_bf16x2(p1.x, p1.y);
             }
-            dk[2 * e] = pack_bf16x2(d0.x, d0.y);
-            dk[2 * e + 1] = pack_bf16x2(d1.x, d1.y);
           }
-          if (!kDQ) tmem_st16(tX + 16 * q, pk);
+          tmem_st16(tX + 16 * q, pk);
           tmem_st16(tX + 64 + 16 * q, dk);
         }
         tmem_st_wait();
