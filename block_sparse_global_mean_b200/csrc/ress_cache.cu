@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kPage) cache_append_kernel(const AppendParams 
   constexpr int kWarps = kPage / 32;
   __shared__ uint32_t s_cont[2 * kWarps + 1];   // token goes on with the run of the one before
   __shared__ uint32_t s_start[kWarps];          // token of the window that starts a run
-  __shared__ float s_amax[kWarps];
+  __shared__ uint32_t s_top[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int which = (int)(blockIdx.x & 1u);
   const int head = (int)((blockIdx.x >> 1) % (unsigned)p.kv_heads);
@@ -297,20 +297,27 @@ __global__ void __launch_bounds__(kPage) cache_append_kernel(const AppendParams 
         if (row0 + 4 * k < n) v[k].load(x + (first + row0 + 4 * k) * stride + col);
         else v[k].zero();
       }
-      float amax = 0.f;
+      // Largest magnitude as bits, which order as the values do, with infinities
+      // and NaN on top; the scale is that of the finite ones.
+      uint32_t top = 0, all = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         float f[8];
         v[k].get(f);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) amax = fmaxf(amax, fabsf(f[u]));
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t b = __float_as_uint(f[u]) & 0x7fffffffu;
+          all = max(all, b);
+          top = max(top, b >= 0x7f800000u ? 0u : b);
+        }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      if (lane == 0) s_amax[warp] = amax;
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (all >= 0x7f800000u) raise_device_error(p.err, RESS_ERR_INVALID_ARG, 105);
+      if (lane == 0) s_top[warp] = top;
       __syncthreads();   // (and every thread has read the old scale)
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) amax = fmaxf(amax, s_amax[w]);
+      for (int w = 0; w < kWarps; ++w) top = max(top, s_top[w]);
+      const float amax = __uint_as_float(top);
       const float now = fmaxf(pow2(scale_exponent(amax)), old);
       const float inv = 1.0f / now;   // exact: a power of two
       uint8_t* dst = cache + ((size_t)page * p.kv_heads + head) * kPage * 64;
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(kPage) cache_append_kernel(const AppendParams 
           *at = e4m3x2(a.x * ratio, a.y * ratio) | e4m3x2(b.x * ratio, b.y * ratio) << 16;
         }
       }
-      __syncthreads();   // s_amax is free again
+      __syncthreads();   // s_top is free again
     }
   }
 }

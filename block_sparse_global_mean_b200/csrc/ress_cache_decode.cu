@@ -3,7 +3,7 @@
 //
 // Bound by reading the pages once (128 bytes a token and head), so everything is
 // laid out for loads: every warp is a worker of its own (ress_sched.cuh) with a
-// private ring of two 64-token chunks, copied by the bulk engine; no warp waits
+// private ring of three 32-token chunks, copied by the bulk engine; no warp waits
 // for another.  A chunk's codes go from shared memory straight into the operand
 // registers of m16n8k16 products: 16 rows (token, query head of the key head)
 // against 64 keys.  At a few rows per key the tensor core's rate is not the
@@ -38,9 +38,10 @@ namespace {
 constexpr int kSms = 148;
 constexpr int kWarps = 12;
 constexpr int kWorkers = kSms * kWarps;
-constexpr int kKeys = 64;                        // keys per chunk
+constexpr int kKeysLog2 = 5;
+constexpr int kKeys = 1 << kKeysLog2;            // keys per chunk
 constexpr int kRows = 16;
-constexpr int kStages = 2;
+constexpr int kStages = 3;
 constexpr uint32_t kHalf = kKeys * 64;           // bytes of keys (values) of a chunk
 constexpr float kScaleLog2 = 1.4426950408889634f * 0.125f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -49,6 +50,7 @@ struct DecodeParams {
   SchedParams sched;
   DeviceError* err;
   int nq, heads, kv_heads, group;
+  int group_inv;       // 65536 / group, rounded up
   long long q_stride;
   const __nv_bfloat16* q;
   __nv_bfloat16* out;
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   uint8_t* ring = &sm->ring[warp][0][0];
   int issued = 0, used = 0;   // copies started and waited for
   bool ok = true;
-  // Column n of an S product holds key `8 j + key_of(n)`: neighbours in a pair
+  // Column n of S product j holds key 8 j + k_row(n): neighbours in a pair
   // and the four pairs differ in parity, so that neither the key loads nor the
   // value loads meet in the same banks more than twice.
   const int k_row = (g & ~1) + (((g >> 1) ^ g) & 1);
@@ -152,8 +154,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int r0 = seg.tile * kRows + g, r1 = r0 + 8;
     const bool live0 = r0 < rows, live1 = r1 < rows;
     const bool upper = seg.tile * kRows + 8 < rows;   // rows 8..15 exist (warp-uniform)
-    const int tok0 = r0 / p.group, tok1 = r1 / p.group;
-    const int head0 = seg.head * p.group + r0 % p.group, head1 = seg.head * p.group + r1 % p.group;
+    // Token and query head of a row: the tile's first, and from there less than
+    // group + 16 rows on, where a 16-bit reciprocal divides exactly.
+    const int tok_a = seg.tile == 0 ? 0 : div_small((long long)seg.tile * kRows, p.group);
+    const int rest = seg.tile * kRows - tok_a * p.group + g;
+    const int step0 = (rest * p.group_inv) >> 16, step1 = ((rest + 8) * p.group_inv) >> 16;
+    const int tok0 = tok_a + step0, tok1 = tok_a + step1;
+    const int head0 = seg.head * p.group + rest - step0 * p.group;
+    const int head1 = seg.head * p.group + rest + 8 - step1 * p.group;
     const size_t row0 = (size_t)(seg.row_start + tok0), row1 = (size_t)(seg.row_start + tok1);
     uint32_t q0[8], q1[8];
     const float qs0 = load_query(p.q + row0 * p.q_stride + head0 * kHeadDim + 16 * t, live0, q0);
@@ -214,13 +222,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         ++used;
         const uint8_t* sk = ring + s * 2 * kHalf;
         const uint8_t* sv = sk + kHalf;
-        const int pos = (base + c) * kKeys;
         const float kscale = __shfl_sync(0xffffffffu, ks, c) * kScaleLog2;
         const float vscale = __shfl_sync(0xffffffffu, vs, c);
 
-        float x[8][4];
+        const int pos = (base + c) * kKeys;
+        float x[4][4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
           const uint4 w = *reinterpret_cast<const uint4*>(sk + (8 * j + k_row) * 64 + 16 * t);
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -235,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const int lim0 = end0 - pos, lim1 = end1 - pos;
         if (__any_sync(0xffffffffu, lim0 < kKeys || lim1 < kKeys)) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             if (8 * j + v_row0 >= lim0) x[j][0] = -INFINITY;
             if (8 * j + v_row1 >= lim0) x[j][1] = -INFINITY;
             if (8 * j + v_row0 >= lim1) x[j][2] = -INFINITY;
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         // Chunk maximum, probabilities, sums.
         float c0 = -INFINITY, c1 = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           c0 = fmax3(c0, x[j][0], x[j][1]);
           c1 = fmax3(c1, x[j][2], x[j][3]);
         }
@@ -258,9 +266,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const float n0 = fmaxf(m0, c0);
         const float u0 = any0 ? -c0 : 0.f;
         float s0 = 0.f, s1 = 0.f;
-        uint32_t pk[8][2];
+        uint32_t pk[4][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float pa = fast_exp2(fmaf(x[j][0], f0, u0)), pb = fast_exp2(fmaf(x[j][1], f0, u0));
           s0 += pa + pb;
           pk[j][0] = pack_f16x2(pa, pb);
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const float n1 = fmaxf(m1, c1);
           const float u1 = any1 ? -c1 : 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             const float pa = fast_exp2(fmaf(x[j][2], f1, u1)), pb = fast_exp2(fmaf(x[j][3], f1, u1));
             s1 += pa + pb;
             pk[j][1] = pack_f16x2(pa, pb);
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j][0] = y[j][1] = y[j][2] = y[j][3] = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
+        for (int kb = 0; kb < 2; ++kb) {
           const uint32_t a[4] = {pk[2 * kb][0], pk[2 * kb][1], pk[2 * kb + 1][0], pk[2 * kb + 1][1]};
           uint2 w[4];
 #pragma unroll
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < 1; ++half) {
       const bool live = half ? live1 : live0;
       if (!live) continue;
       const float m = half ? m1 : m0, l = half ? l1 : l0;
@@ -416,6 +424,7 @@ ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st)
   p.heads = c.heads;
   p.kv_heads = c.kv_heads;
   p.group = c.group;
+  p.group_inv = (65535 + c.group) / c.group;
   p.q_stride = c.q_stride;
   p.q = c.q;
   p.out = c.out;
@@ -443,9 +452,9 @@ ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st)
   p.sched.row_mult = c.group;
   p.sched.tile_rows = kRows;
   p.sched.mult = 1;
-  p.sched.chunk = kKeys;
-  p.sched.item_cost = kKeys;
-  p.sched.min_share = 2 * kKeys;
+  p.sched.chunk_log2 = kKeysLog2;
+  p.sched.item_cost = 64;
+  p.sched.min_share = 128;
   p.sched.grid = kWorkers;
   static std::atomic<uint64_t> allowed{0};
   if (ress_status s =

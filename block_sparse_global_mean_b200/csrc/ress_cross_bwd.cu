@@ -702,7 +702,7 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
     s.tile_rows = dq ? p.tps : 128;
     s.mult = dq ? 1 : g.group;
     s.row_mult = 1;
-    s.chunk = kChunk;
+    s.chunk_log2 = kChunkLog2;
     s.item_cost = kItemCost;
     s.min_share = kMinShare;
     s.grid = kSms;

@@ -28,7 +28,8 @@
 
 namespace ress {
 
-constexpr int kChunk = 128;       // columns per chunk of the tensor-core walks
+constexpr int kChunkLog2 = 7;
+constexpr int kChunk = 1 << kChunkLog2;   // columns per chunk of the tensor-core walks
 constexpr int kItemCost = 256;    // an item's fixed work there, in units of a column
 constexpr int kMinShare = 512;    // smallest share worth a CTA
 
@@ -46,7 +47,8 @@ struct SchedParams {
   int tile_rows;              // item rows of a tile
   int mult;                   // passes over the columns (query heads of a key head)
   int step;                   // the cache's step mask (0: none); needs row_mult 1
-  int chunk, item_cost, min_share;
+  int chunk_log2;             // columns per chunk
+  int item_cost, min_share;   // units
   int grid;                   // workers
   long long max_len;          // largest valid entry of `lengths`
 };
@@ -65,6 +67,20 @@ __device__ __forceinline__ SeqRange sched_cols(const SchedParams& p, int b) {
   return SeqRange{0, len, len};
 }
 
+// floor(a / b) for a >= 0, b > 0 and a quotient below 2^24, by an estimate in
+// float32 and its correction: a fraction of the instructions of a 64-bit division,
+// which matter in the first microsecond of a kernel, when none is cached.
+__device__ __forceinline__ int div_small(long long a, long long b) {
+  int q = __float2int_rz(__fdividef(__ll2float_rz(a), __ll2float_rz(b)));
+  long long r = a - (long long)q * b;
+  while (r < 0) --q, r += b;
+  while (r >= b) ++q, r -= b;
+  return q;
+}
+__device__ __forceinline__ int ceil_small(long long a, long long b) {
+  return div_small(a + b - 1, b);
+}
+
 // Items of one sequence: tile t of any head costs base + slope * t units.  A
 // step mask makes later tiles longer; its staircase is taken as a line, which
 // moves the borders of the shares but not what is computed.
@@ -72,19 +88,22 @@ struct SeqCost {
   int tiles;
   long long base, slope;
   __device__ __forceinline__ long long before(long long t) const {
-    return base * t + slope * (t * (t - 1) / 2);
+    return base * t + (slope == 0 ? 0 : slope * (t * (t - 1) / 2));
   }
   __device__ __forceinline__ long long most() const { return base + slope * (tiles - 1); }
-  __device__ __forceinline__ int pieces(long long share) const;
+  __device__ __forceinline__ int pieces(long long share) const { return ceil_small(most(), share); }
 };
+__device__ __forceinline__ long long sched_chunks_of(const SchedParams& p, int cols) {
+  return (long long)((cols + (1 << p.chunk_log2) - 1) >> p.chunk_log2) * p.mult;
+}
 __device__ __forceinline__ SeqCost sched_cost(const SchedParams& p, const SeqRange& r,
                                               const SeqRange& c) {
-  SeqCost s{(int)(((long long)r.rows * p.row_mult + p.tile_rows - 1) / p.tile_rows), 0, 0};
+  SeqCost s{ceil_small((long long)r.rows * p.row_mult, p.tile_rows), 0, 0};
   if (p.step > 0 && p.step < r.rows) {
     s.base = p.item_cost + max(c.valid - r.rows, 0) + p.tile_rows;
     s.slope = p.tile_rows;
   } else {
-    s.base = p.item_cost + (long long)((c.valid + p.chunk - 1) / p.chunk) * p.chunk * p.mult;
+    s.base = p.item_cost + (sched_chunks_of(p, c.valid) << p.chunk_log2);
   }
   return s;
 }
@@ -94,17 +113,7 @@ __device__ __forceinline__ SeqCost sched_cost(const SchedParams& p, int b) {
 
 // Chunks whose unit lies before unit x of an item.
 __device__ __forceinline__ long long sched_chunks_before(const SchedParams& p, long long x) {
-  return x <= p.item_cost ? 0 : (x - p.item_cost + p.chunk - 1) / p.chunk;
-}
-
-// a / b for a >= 0, b > 0, in 32 bits where they fit (a third of the time).
-__device__ __forceinline__ long long div_pos(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
-  return a / b;
-}
-
-__device__ __forceinline__ int SeqCost::pieces(long long share) const {
-  return (int)div_pos(most() + share - 1, share);
+  return x <= p.item_cost ? 0 : (x - p.item_cost + (1 << p.chunk_log2) - 1) >> p.chunk_log2;
 }
 
 enum SchedMode { kLine, kPieces, kRounds };
@@ -126,95 +135,87 @@ struct SchedWalk {
   int b, worker;
 };
 
-// Pieces of the sequences from `b0` on, one per lane.
+// Pieces of a sequence, or its units on the line.
 __device__ __forceinline__ long long sched_count(const SchedParams& p, const SeqCost& cost,
                                                  SchedMode mode, long long share) {
   if (cost.tiles == 0) return 0;
-  const long long n = (long long)cost.tiles * p.heads;
-  return mode == kLine     ? cost.before(cost.tiles) * p.heads
-         : mode == kPieces ? n * cost.pieces(share)
-                           : n;
+  return mode == kLine ? cost.before(cost.tiles) * p.heads
+                       : (long long)cost.tiles * p.heads * cost.pieces(share);
+}
+
+// Upper bound of total / parts, within a millionth of it.
+__device__ __forceinline__ long long sched_even(long long total, int parts) {
+  return __float2ll_ru(__ll2float_ru(total) * 1.000001f / (float)parts) + 1;
 }
 
 // The plan, and where `worker` begins (at == ub: nowhere).  Called by a warp.
 __device__ __forceinline__ SchedPlan sched_begin(const SchedParams& p, int worker, SchedWalk* walk) {
   const int lane = threadIdx.x & 31;
+  const bool few = p.seqs <= 32;   // a sequence per lane: its cost stays in registers
   SeqCost cost{0, 0, 0};
-  long long units = 0, items = 0, cap = 0, least = 0x7fffffffffffffffll, most = 0;
-  bool flat = true;
+  long long units = 0;
+  int items = 0;
   for (int b = lane; b < p.seqs; b += 32) {
     cost = sched_cost(p, b);
-    const long long n = (long long)cost.tiles * p.heads;
-    items += n;
+    items += cost.tiles * p.heads;
     units += cost.before(cost.tiles) * p.heads;
-    cap += n * cost.most();
-    if (n > 0) {
-      least = min(least, cost.base);
-      most = max(most, cost.base);
-      flat = flat && cost.slope == 0;
-    }
   }
-  items = warp_sum(items);
+  const bool none = items == 0;
   units = warp_sum(units);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  }
-  flat = __all_sync(0xffffffffu, flat) && least == most;
+  items = __reduce_add_sync(0xffffffffu, items);
   walk->worker = worker;
   walk->at = walk->ub = 0;
-  SchedPlan plan{kLine, max(div_pos(units + p.grid - 1, p.grid), (long long)p.min_share),
-                 (int)min(items, 0x7fffffffll), 1};
+  SchedPlan plan{kLine, max(sched_even(units, p.grid), (long long)p.min_share), items, 1};
   if (items == 0) return plan;
-  if (flat && p.seqs <= 32 && items < (1 << 24)) {   // (sched_next looks through the sequences)
-    // Each lane tries a number of pieces: 1 .. 30, and those that fill one or
-    // two rounds.  More than two rounds only of whole items (a worker has two
-    // partial slots).
-    const int n = (int)items, chunks = (int)min(div_pos(most - p.item_cost, p.chunk), 1ll << 24);
-    int ns = lane < 30 ? lane + 1 : (lane - 29) * p.grid / n;
+  const int one = __ffs((int)__ballot_sync(0xffffffffu, !none)) - 1;
+  const long long base1 = __shfl_sync(0xffffffffu, cost.base, one);
+  if (few && __all_sync(0xffffffffu, none || (cost.base == base1 && cost.slope == 0)) &&
+      items < (1 << 20)) {
+    // Equal items.  Each lane tries a number of pieces: 1 .. 30, and those that
+    // fill one or two rounds.  More than two rounds only of whole items (a worker
+    // has two partial slots).
+    const int chunks = (int)min((base1 - p.item_cost) >> p.chunk_log2, 1ll << 20);
+    int ns = lane < 30 ? lane + 1 : div_small((long long)(lane - 29) * p.grid, items);
     ns = max(1, min(ns, chunks));
-    const int rounds = (int)div_pos((long long)n * ns + p.grid - 1, p.grid);
-    long long t = (long long)rounds * (p.item_cost + (long long)((chunks + ns - 1) / ns) * p.chunk);
-    if (ns > 1 && rounds > 2) t = 0x7fffffffffffffll;
-    long long best = (t << 8) + ns % 256;   // the fewest pieces of the shortest
-    if (ns > 255) best = (t << 8) + 255;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = min(best, __shfl_xor_sync(0xffffffffu, best, o));
-    // The line costs an item's fixed work more, and is fully even.
-    if ((best >> 8) <= plan.share + (plan.share >> 4) + p.item_cost) {
-      const unsigned who =
-          __ballot_sync(0xffffffffu, (t << 8) + (ns > 255 ? 255 : ns) == best);
-      plan.ns = __shfl_sync(0xffffffffu, ns, __ffs((int)who) - 1);
+    const int rounds = ceil_small((long long)items * ns, p.grid);
+    // Rounds times an item's fixed work and its chunks, both in chunks.
+    long long t = (long long)rounds * (((p.item_cost - 1) >> p.chunk_log2) + 1 + ceil_small(chunks, ns));
+    if (ns > 1 && rounds > 2) t = 0xfffffff;
+    // The fewest pieces of the shortest.
+    const unsigned key = (unsigned)min(t, 0xfffffffll);
+    const unsigned best = __reduce_min_sync(0xffffffffu, key);
+    const int least = (int)__reduce_min_sync(0xffffffffu, key == best ? (unsigned)ns : 0xffffffffu);
+    // The line is fully even, but costs an item's fixed work more.
+    if (((long long)best << p.chunk_log2) <= plan.share + (plan.share >> 4) + p.item_cost) {
+      plan.ns = least;
       plan.mode = kRounds;
+      walk->at = worker;
+      walk->ub = (long long)items * least;
+      return plan;
     }
   }
-  if (plan.mode != kRounds && 2 * items <= p.grid && units <= (long long)p.grid * 16 * p.chunk) {
+  if (2 * items <= p.grid && units <= ((long long)p.grid * 16 << p.chunk_log2)) {
     // Shares that grow until all pieces fit.  sum ceil(cost / share) <= sum cost /
     // share + items, so the last one is sure to.
     plan.mode = kPieces;
-    cap = warp_sum(cap);
-    for (int i = 0; i < 3; ++i) {
-      long long n = 0;
+    for (int i = 0; i < 9; ++i) {
+      int n = 0;
+      long long cap = 0;
       for (int b = lane; b < p.seqs; b += 32) {
-        if (p.seqs > 32) cost = sched_cost(p, b);
-        n += sched_count(p, cost, kPieces, plan.share);
+        if (!few) cost = sched_cost(p, b);
+        n += (int)sched_count(p, cost, kPieces, plan.share);
+        cap += (long long)cost.tiles * p.heads * cost.most();
       }
-      if (warp_sum(n) <= p.grid) break;
-      plan.share = i < 2 ? plan.share + (plan.share >> 2)
-                         : max(plan.share, div_pos(cap + p.grid - items - 1, p.grid - items));
+      if (__reduce_add_sync(0xffffffffu, n) <= p.grid) break;
+      plan.share = i < 7 ? plan.share + (plan.share >> 4)
+                         : max(plan.share, sched_even(warp_sum(cap), p.grid - items));
     }
   }
   const long long unit = plan.mode == kLine ? worker * plan.share : worker;
-  if (plan.mode == kRounds) {
-    walk->at = unit;
-    walk->ub = items * plan.ns;
-    return plan;
-  }
   long long base = 0;
   for (int b0 = 0; b0 < p.seqs; b0 += 32) {
     const int b = b0 + lane;
-    if (p.seqs > 32 && b < p.seqs) cost = sched_cost(p, b);
+    if (!few && b < p.seqs) cost = sched_cost(p, b);
     const long long n = b < p.seqs ? sched_count(p, cost, plan.mode, plan.share) : 0;
     long long incl = n;
 #pragma unroll
@@ -246,11 +247,11 @@ __device__ __forceinline__ SchedItem sched_item(const SeqCost& s, long long seq_
   const long long per_head = s.before(s.tiles);
   const long long r = u - seq_start;
   SchedItem it;
-  it.head = (int)div_pos(r, per_head);
+  it.head = div_small(r, per_head);
   const long long x = r - it.head * per_head;
   long long t;
   if (s.slope == 0) {
-    t = div_pos(x, s.base);
+    t = div_small(x, s.base);
   } else {   // last t with before(t) <= x
     long long lo = 0, hi = s.tiles - 1;
     while (lo < hi) {
@@ -279,18 +280,16 @@ struct Segment {
 
 __device__ __forceinline__ long long sched_chunks(const SchedParams& p, const SeqRange& r,
                                                   const SeqRange& c, int tile) {
-  if (p.step > 0) {
-    const int last = min((tile + 1) * p.tile_rows, r.rows) - 1;
-    return (step_end(c.valid, r.rows, last, p.step) + p.chunk - 1) / p.chunk;
-  }
-  return (long long)((c.valid + p.chunk - 1) / p.chunk) * p.mult;
+  if (p.step == 0) return sched_chunks_of(p, c.valid);
+  const int last = min((tile + 1) * p.tile_rows, r.rows) - 1;
+  return (step_end(c.valid, r.rows, last, p.step) + (1 << p.chunk_log2) - 1) >> p.chunk_log2;
 }
 
 // Piece `piece` of `ns` of an item's chunks.
 __device__ __forceinline__ void sched_piece(Segment& g, long long chunks, int piece, int ns) {
-  const unsigned q = (unsigned)chunks / (unsigned)ns, rest = (unsigned)chunks - q * (unsigned)ns;
-  g.c0 = (int)(q * piece + min((unsigned)piece, rest));   // the first `rest` get one more
-  g.c1 = g.c0 + (int)(q + ((unsigned)piece < rest ? 1u : 0u));
+  const int q = ns == 1 ? (int)chunks : div_small(chunks, ns), rest = (int)chunks - q * ns;
+  g.c0 = q * piece + min(piece, rest);   // the first `rest` get one more
+  g.c1 = g.c0 + q + (piece < rest ? 1 : 0);
   g.kind = ns == 1 ? 1 : 2;
   if (piece == 0 && ns > 1) g.parts = ns;
 }
@@ -303,10 +302,9 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, const SchedP
   if (w.at >= w.ub) return g;
   int piece = 0, item = 0;
   if (plan.mode == kRounds) {   // the sequence of the item: they differ in their tiles alone
-    const int at = (int)w.at;
-    piece = (int)div_pos(w.at, plan.items);
-    item = at - piece * plan.items;
-    g.slot = (int)div_pos(w.at, p.grid) & 1;
+    piece = plan.ns == 1 ? 0 : div_small(w.at, plan.items);
+    item = (int)w.at - piece * plan.items;
+    g.slot = w.at >= p.grid ? 1 : 0;   // of whole items, where there may be more rounds, unused
     g.stride = plan.items;
     w.at += p.grid;
     for (w.b = 0;; ++w.b) {
@@ -323,11 +321,11 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, const SchedP
       if (plan.mode == kPieces) {
         ns = s.pieces(plan.share);
         const int at = (int)(w.at - w.seq_start);   // at most grid, as ns
-        item = at / ns;
+        item = div_small(at, ns);
         piece = at - item * ns;
         w.at = w.ub;
       }
-      g.head = item / s.tiles;
+      g.head = div_small(item, s.tiles);
       g.tile = item - g.head * s.tiles;
       sched_piece(g, sched_chunks(p, r, c, g.tile), piece, ns);
     } else {
@@ -348,7 +346,7 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, const SchedP
       g.kind = x0 == 0 && x1 == it.cost ? 1 : 2;
       if (x0 == 0 && g.kind == 2) {   // an end or middle is a worker's first, a beginning its last
         g.slot = 1;
-        g.parts = (int)div_pos(it.start + it.cost - 1, plan.share) - w.worker + 1;
+        g.parts = div_small(it.start + it.cost - 1, plan.share) - w.worker + 1;
       }
       w.at = it.start + x1;
     }

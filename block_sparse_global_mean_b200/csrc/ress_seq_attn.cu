@@ -753,7 +753,7 @@ static ress_status launch_seq(const CrossParams& c, bool cache, void* ws, cudaSt
   p.sched.heads = c.kv_heads;
   p.sched.mult = 1;
   p.sched.row_mult = 1;
-  p.sched.chunk = kChunk;
+  p.sched.chunk_log2 = kChunkLog2;
   p.sched.item_cost = kItemCost;
   p.sched.min_share = kMinShare;
   p.sched.grid = kSms;

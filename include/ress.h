@@ -605,8 +605,9 @@ ress_status ress_cache_plan(const ress_cache_shape* shape, const int32_t* added,
  *
  *   A page that appears in two runs of one call gets an undefined content
  *   (two runs write it at once); slots outside the pool are skipped and
- *   flagged (RESS_ERR_BAD_INDEX, detail 104).  Values must be finite: a NaN
- *   becomes the NaN code, an infinity the largest number of its scale.
+ *   flagged (RESS_ERR_BAD_INDEX, detail 104).  Values must be finite: one that
+ *   is not is flagged (RESS_ERR_INVALID_ARG, detail 105) and does not count for
+ *   the scale; its code is NaN, or for an infinity the largest number.
  *   shape->requests and max_pages are not used.  One launch, no workspace.
  */
 ress_status ress_cache_append(const ress_cache_shape* shape, const void* k, const void* v,
@@ -644,8 +645,9 @@ size_t ress_cache_attn_workspace_bytes(const ress_cache_shape* shape, int32_t he
  *   out       [tokens][heads][64] bf16;  lse [heads][tokens] float32 or NULL.
  *   workspace ress_cache_attn_workspace_bytes() bytes, 256-byte aligned.
  *   Codes and queries are multiplied exactly; probabilities enter P V as
- *   bf16, their sums and lse are float32.  Cells behind lengths[r] are never
- *   used as numbers.
+ *   bf16 or f16, their sums and lse are float32.  Cells behind lengths[r] are
+ *   never used as numbers; a NaN code before them may count as 480 (the append
+ *   that made it was flagged).  Scales must be powers of two from 2^-100 to 2^119.
  */
 ress_status ress_cache_attn(const ress_cache_shape* shape, int32_t heads, int32_t tokens,
                             const void* q, int64_t q_stride, const void* k_cache,

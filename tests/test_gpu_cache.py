@@ -250,7 +250,7 @@ def test_append_is_exact(page, heads, starts, counts, dtype, ress_gpu):
 def test_append_at_the_edges_of_its_number_range(ress_gpu):
     """Zeros, values below the smallest scale, exact multiples of 448, the
     smallest code, a page whose scale grows by more than e4m3 can hold, and
-    NaN and infinity, which stay in their own cells."""
+    NaN and infinity, which are flagged and stay in their own cells."""
     page, heads = 64, 4
     rows = torch.zeros(6, heads, 64)
     rows[0, 1] = 448.0
@@ -268,10 +268,15 @@ def test_append_at_the_edges_of_its_number_range(ress_gpu):
     cache = _filled_cache(ress_gpu, 1, 1, page, seed=4)
     x = torch.ones(2, 1, 64)
     x[0, 0, 5], x[1, 0, 7] = float("nan"), float("nan")
+    x[1, 0, 9] = float("-inf")
     ress_gpu.ress_cache_append(x.cuda(), x.cuda(), _i32([0, 1]), cache)
-    got = np64(cache.k)[0, 0, :2] * np64(cache.k_scale)[0, 0]
-    want = np64(x)[:, 0]
+    status, detail = ress_gpu.ress_check_device_errors()
+    assert status == ress_gpu.RESS_ERR_INVALID_ARG and detail == 105
+    scale = np64(cache.k_scale)[0, 0]
+    assert scale == 2.0 ** -8                    # of the ones among them
+    got, want = np64(cache.k)[0, 0, :2] * scale, np64(x)[:, 0]
     assert np.array_equal(np.isnan(got), np.isnan(want))
+    want[1, 9] = -448 * scale
     assert np.array_equal(got[~np.isnan(got)], want[~np.isnan(want)])
 
 
