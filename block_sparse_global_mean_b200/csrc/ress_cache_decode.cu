@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
 #pragma unroll
-    for (int half = 0; half < 1; ++half) {
+    for (int half = 0; half < 2; ++half) {
       const bool live = half ? live1 : live0;
       if (!live) continue;
       const float m = half ? m1 : m0, l = half ? l1 : l0;
