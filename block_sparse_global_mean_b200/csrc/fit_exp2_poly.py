@@ -1,16 +1,14 @@
-"""Fits the polynomials that the attention kernels use for part of their
-exponentials: 2^f on f in [-1/2, 1/2], degree 3 (exp2_poly2) or 4
-(exp2_poly4), minimising the maximum relative error.
+"""Fits the polynomial that the attention kernel uses for part of its
+exponentials: 2^f on f in [-1/2, 1/2], degree 3, minimising the maximum
+relative error.
 
 Method: Lawson's algorithm (iteratively reweighted least squares converging
 to the minimax fit) on a dense grid, then a check of the float32 Horner
 evaluation.  The kernel combines it with the range reduction
 2^x = 2^n * 2^f, n = round(x), f = x - n.
 
-    python fit_exp2_poly.py [degree]     # prints the coefficients and the error
+    python fit_exp2_poly.py      # prints the coefficients and the error
 """
-
-import sys
 
 import numpy as np
 
@@ -39,7 +37,7 @@ def horner_f32(c, f):
 
 
 if __name__ == "__main__":
-    c = fit(int(sys.argv[1]) if len(sys.argv) > 1 else 3)
+    c = fit()
     f = np.linspace(-0.5, 0.5, 200001)
     rel = np.abs(horner_f32(c, f).astype(np.float64) / 2.0 ** f - 1.0).max()
     for k, v in enumerate(c.astype(np.float32)):

@@ -172,10 +172,16 @@ bool make_rows_map(CUtensorMap* map, const void* base, int heads, int64_t rows,
   const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)row_stride * 2};
   const cuuint32_t box[3] = {(cuuint32_t)kHeadDim, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = CUDA_ERROR_INVALID_CONTEXT;
+  for (int i = 0; i < 2 && r == CUDA_ERROR_INVALID_CONTEXT; ++i) {
+    // A driver call in a thread that has made no runtime call yet finds no
+    // context; choosing the device that is current anyway binds its own.
+    int dev = 0;
+    if (i == 1 && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)) break;
+    r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
   if (r != CUDA_SUCCESS)
     snprintf(g_last_cuda_error, sizeof(g_last_cuda_error),
              "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);

@@ -355,7 +355,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     for (int half = 0; half < 2; ++half) {
       const bool live = half ? live1 : live0;
       if (!live) continue;
-      const float m = half ? m1 : m0, l = half ? l1 : l0;
+      const float l = half ? l1 : l0;
+      float m = half ? m1 : m0;
+      if (m == -INFINITY && l != l) m = 0.f;   // NaN logits move no maximum, but reach the sum
       const bool empty = m == -INFINITY;
       if (seg.kind == 1) {
         const float inv = empty ? 0.f : 1.0f / l;

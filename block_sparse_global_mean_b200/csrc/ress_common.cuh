@@ -463,25 +463,6 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
                      __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
 }
 
-// 2^x for a pair on the FMA and integer pipes, as exp2_poly2 but of degree 4
-// (coefficients from fit_exp2_poly.py; largest relative error 2.8e-6, mean 4e-8),
-// for sums of the unrounded values.
-__device__ __forceinline__ float2 exp2_poly4(float2 x) {
-  constexpr float kShift = 12582912.0f;   // 1.5 * 2^23
-  x.x = fmaxf(x.x, -126.0f);
-  x.y = fmaxf(x.y, -126.0f);
-  const float2 t = fadd2(x, make_float2(kShift, kShift));
-  const float2 n = fadd2(t, make_float2(-kShift, -kShift));
-  const float2 f = ffma2(n, make_float2(-1.0f, -1.0f), x);
-  float2 q = ffma2(make_float2(0.00957007986f, 0.00957007986f), f,
-                   make_float2(0.0559178367f, 0.0559178367f));
-  q = ffma2(q, f, make_float2(0.240247443f, 0.240247443f));
-  q = ffma2(q, f, make_float2(0.693121791f, 0.693121791f));
-  q = ffma2(q, f, make_float2(0.999999285f, 0.999999285f));
-  return make_float2(__int_as_float(__float_as_int(q.x) + (__float_as_int(t.x) << 23)),
-                     __int_as_float(__float_as_int(q.y) + (__float_as_int(t.y) << 23)));
-}
-
 // acc + (bf16 in the low / high half of `pk`), accumulated in float32
 // (sm_100 mixed-precision add).
 __device__ __forceinline__ float add_bf16_lo(uint32_t pk, float acc) {

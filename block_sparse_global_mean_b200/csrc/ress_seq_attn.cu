@@ -492,8 +492,7 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
           for (int e = 0; e < 16; ++e) {
             const float2 sv = make_float2(__uint_as_float(r[q][2 * e]), __uint_as_float(r[q][2 * e + 1]));
             const float2 x = ffma2(sv, scale2, neg_m2);
-            const float2 pe = ((e & 7) == 7) ? exp2_poly4(x)
-                                             : make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
             if (e & 1) sum_b = fadd2(sum_b, pe);
             else sum_a = fadd2(sum_a, pe);
             pk[e] = pack_bf16x2(pe.x, pe.y);
@@ -545,6 +544,8 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
       if (ok && n_ch > 0) ok = warp_wait(bar_o, n_o & 1, abortf, p.err, 133);
       if (ok && writes) {
         tc_fence_after();
+        // Logits that are NaN move no maximum, but reach the sum.
+        if (m == -INFINITY && l != l) m = 0.f;
         const bool empty = !real || m == -INFINITY;
         const float inv = kind != 1 ? 1.f : empty ? 0.f : 1.0f / l;
         const size_t part = ((size_t)blockIdx.x * 2 + g.slot) * C::rows +

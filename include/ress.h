@@ -498,7 +498,8 @@ size_t ress_cross_bwd_workspace_bytes(const ress_cross_shape* shape);
  *              (NULL when that is 0).
  *   Contractions on bf16 operands with float32 accumulation; probabilities
  *   enter P V as bf16, their sum and lse are float32 sums of the unrounded
- *   ones.  Results do not depend on the run: no atomics add numbers.
+ *   ones.  Results do not depend on the run: no atomics add numbers.  Outputs
+ *   must not overlap inputs.
  */
 ress_status ress_cross_attn(const ress_cross_shape* shape, const void* q, const void* k,
                             const void* v, const int32_t* q_offsets, const int32_t* kv_offsets,
@@ -519,8 +520,8 @@ ress_status ress_cross_attn(const ress_cross_shape* shape, const void* q, const 
  *   dout       [nq][heads][64] bf16.
  *   dq         [nq][heads][64] bf16; dk, dv [nk][kv_heads][64] bf16.
  *   workspace  ress_cross_bwd_workspace_bytes(shape) bytes, 256-byte aligned.
- *   P and dS enter their products as bf16; all sums are float32 in a fixed
- *   order.
+ *   P enters its product as bf16, dS as bf16 for dk and as two bf16 numbers
+ *   (16 bits) for dq; all sums are float32 in a fixed order.
  */
 ress_status ress_cross_attn_bwd(const ress_cross_shape* shape, const void* q, const void* k,
                                 const void* v, const void* out, const float* lse,

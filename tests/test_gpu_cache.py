@@ -468,6 +468,69 @@ def test_rows_of_no_request_are_left_as_they_were(ress_gpu):
     assert (lse[:, :4] == 7).all() and (lse[:, 9:] == 7).all()
 
 
+@pytest.mark.parametrize("queries", [1, 150])
+def test_a_nan_query_comes_out(queries, ress_gpu):
+    q, cache, table, off = make_requests(ress_gpu, [300, 90], [queries] * 2, 64, 4, 2, seed=41)
+    args = cache, _i32(table), _i32([300, 90]), _i32(off)
+    want, wlse = ress_gpu.ress_cache_attn(q.cuda(), *args)
+    q[queries, 3, 17] = float("nan")
+    out, lse = ress_gpu.ress_cache_attn(q.cuda(), *args)
+    _ok(ress_gpu)
+    assert out[queries, 3].isnan().all() and lse[3, queries].isnan()
+    out[queries, 3], lse[3, queries] = want[queries, 3], wlse[3, queries]
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@pytest.mark.parametrize("queries", [1, 200])
+def test_pools_beyond_4_gb(queries, ress_gpu):
+    """Pages whose byte offsets pass 2^32: the same tokens in the last pages of a
+    large pool and in a small one."""
+    pages, heads = 70000, 16                           # 4.6 GB of codes each
+    big, small = ress_gpu.make_cache(pages, heads, 64), ress_gpu.make_cache(8, heads, 64)
+    x = torch.randn(200, 2, heads, 64, generator=torch.Generator().manual_seed(2)).to(
+        torch.bfloat16).cuda()
+    ids = torch.tensor([[pages - 1, pages - 3, 5, pages - 2], [0, 1, 2, 3]])
+    q = torch.randn(queries, heads, 64, generator=torch.Generator().manual_seed(3)).to(
+        torch.bfloat16).cuda()
+    got = []
+    for cache, row in ((big, ids[0]), (small, ids[1])):
+        t = torch.arange(200)
+        ress_gpu.ress_cache_append(x[:, 0], x[:, 1], _i32((row[t // 64] * 64 + t % 64).tolist()),
+                                   cache)
+        got.append(ress_gpu.ress_cache_attn(q, cache, _i32([row.tolist()]), _i32([200]),
+                                            _i32([0, queries])))
+    _ok(ress_gpu)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    for a, b in zip(big, small):
+        assert torch.equal(a[ids[0].cuda()].float(), b[:4].float())
+
+
+def test_threads_that_share_a_stream(ress_gpu):
+    """Calls from several threads on one stream: each has its own workspace."""
+    import threading
+    data = [make_requests(ress_gpu, [3000, 500], [n] * 2, 64, 8, 4, seed=50 + n) for n in (1, 90)]
+    dev = [(q.cuda(), c, _i32(t), _i32([3000, 500]), _i32(o)) for q, c, t, o in data]
+    want = [ress_gpu.ress_cache_attn(*a) for a in dev]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(20):
+            got[i].append(ress_gpu.ress_cache_attn(*dev[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    _ok(ress_gpu)
+    for i in (0, 1):
+        assert len(got[i]) == 20
+        for o, l in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
 # ------------------------------------------------------------------------------------------
 # the three together
 # ------------------------------------------------------------------------------------------

@@ -6,8 +6,7 @@ rounded to bf16 (at most 2^-8 relative) while the normaliser is not rounded, so
 |out - ref| <= 2^-8 * sum_t p_t |v_t| + 2^-8 |out| (the output's own rounding)
 + 2^-12 * sum_t p_t |v_t| (exponentials to 2^-14, float32 sums).  lse: logits are
 float32 sums of 64 exact products (|error| <= 64 * 2^-24 * sum |q k| / 8, below
-2^-14 for sums up to 64), the exponentials' 2^-14 averages out, and lg2 is good
-to 2^-20: 1e-4 + 1e-5 |lse|.
+2^-14 for sums up to 64), and ex2 and lg2 are good to 2^-20: 1e-4 + 1e-5 |lse|.
 Gradients: P and dS enter their products rounded to bf16, so
 |dv - ref| <= (2^-8 + 2^-12) sum_i P |dout| + 2^-8 |dv|, and
 |dk - ref| <= (2^-8 + 2^-12) sum_i |dS| |q| / 8 + 2^-8 |dk| + 2^-13 sum_i P N |q| / 8
@@ -248,6 +247,31 @@ def test_infinities_and_nan_of_masked_keys_stay_there(ress_gpu):
     for name, t in zip(("dq", "dk", "dv"), grads):
         close(t, ref, name)
     assert (grads[1][170:] == 0).all() and (grads[2][170:] == 0).all()
+
+
+@pytest.mark.parametrize("nq,nk", [(3, 20), (40, 3000), (700, 400)])
+def test_nan_that_is_attended_to_comes_out(nq, nk, ress_gpu):
+    """A NaN in a query row or in a key reaches every output that depends on it,
+    and a NaN value its dimension of them; other heads and rows stay as they were."""
+    q, k, v, _ = make([nq], [nk], 4, 2, seed=11)
+    want, wlse = ress_gpu.ress_cross_attn(q.cuda(), k.cuda(), v.cuda())
+    a, b, c = (t.clone() for t in (q, k, v))
+    a[1, 1, 5] = float("nan")            # query head 1 of token 1
+    b[nk - 2, 1, 60] = float("nan")      # key head 1: query heads 2 and 3
+    c[7, 0, 9] = float("nan")            # value head 0: query heads 0 and 1
+    out, lse = ress_gpu.ress_cross_attn(a.cuda(), b.cuda(), c.cuda())
+    _ok(ress_gpu)
+    bad = torch.zeros(out.shape, dtype=torch.bool)
+    bad[1, 1] = True
+    bad[:, 2:] = True
+    bad[:, :2, 9] = True
+    assert torch.equal(out.isnan().cpu(), bad)
+    assert torch.equal(out.cpu()[~bad], want.cpu()[~bad])
+    lbad = torch.zeros(lse.shape, dtype=torch.bool)
+    lbad[1, 1] = True
+    lbad[2:] = True
+    assert torch.equal(lse.isnan().cpu(), lbad)
+    assert torch.equal(lse.cpu()[~lbad], wlse.cpu()[~lbad])
 
 
 def test_large_and_flat_logits(ress_gpu):
