@@ -437,21 +437,18 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
         tc_fence_after();
         uint32_t r[4][32];
         tmem_ld32(tX, r[0]);
-        tmem_ld32(tX + 32, r[1]);
-        tmem_ld32(tX + 64, r[2]);
-        tmem_ld32(tX + 96, r[3]);
         // Own view of the chunk (already complete: X needed it).
         if ((!kDQ || left < kChunk) &&
             !warp_wait(bar_bf + 8 * st, (kc / kStages) & 1, abortf, p.err, 171)) {
           ok = false;
           break;
         }
-        tmem_ld_wait_regs(r[0]);
-        tmem_tie_regs(r[1]);
-        tmem_tie_regs(r[2]);
-        tmem_tie_regs(r[3]);
+        // Each piece of X (and below of Y) is on its way while the one before it
+        // is worked on.
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          tmem_ld_wait_regs(r[q]);
+          if (q < 3) tmem_ld32(tX + 32 * (q + 1), r[q + 1]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float4 nl4 = make_float4(nl_row, nl_row, nl_row, nl_row);
@@ -462,12 +459,10 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
             const float2 x1 = ffma2(make_float2(__uint_as_float(r[q][4 * e + 2]),
                                                 __uint_as_float(r[q][4 * e + 3])),
                                     scale2, make_float2(nl4.z, nl4.w));
-            const float2 p0 = make_float2(fast_exp2(x0.x), fast_exp2(x0.y));
-            const float2 p1 = make_float2(fast_exp2(x1.x), fast_exp2(x1.y));
-            r[q][4 * e] = __float_as_uint(p0.x);
-            r[q][4 * e + 1] = __float_as_uint(p0.y);
-            r[q][4 * e + 2] = __float_as_uint(p1.x);
-            r[q][4 * e + 3] = __float_as_uint(p1.y);
+            r[q][4 * e] = __float_as_uint(fast_exp2(x0.x));
+            r[q][4 * e + 1] = __float_as_uint(fast_exp2(x0.y));
+            r[q][4 * e + 2] = __float_as_uint(fast_exp2(x1.x));
+            r[q][4 * e + 3] = __float_as_uint(fast_exp2(x1.y));
           }
         }
         if (!warp_wait(bar_y + 8u * (uint32_t)par, ph, abortf, p.err, 172)) {
@@ -494,40 +489,48 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
           }
           fence_proxy_async_smem();
         }
+        uint32_t y[2][16];
+        tmem_ld16(tY, y[0]);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint32_t y[32], pk[16], dk[16];
-          tmem_ld32(tY + 32 * q, y);
-          tmem_ld_wait_regs(y);
-          if (q == 3) {
-            tc_fence_before();
-            mbar_arrive(bar_yf + 8u * (uint32_t)par);
-          }
-          if (left < kChunk) {
+          uint32_t pk[16], dk[16];
 #pragma unroll
-            for (int u = 0; u < 32; ++u)
-              if (32 * q + u >= left) y[u] = 0u;
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float4 nd4 = make_float4(nd_row, nd_row, nd_row, nd_row);
-            if (!kDQ) nd4 = reinterpret_cast<const float4*>(ctl->nd[st])[8 * q + e];
-            const float2 p0 = make_float2(__uint_as_float(r[q][4 * e]), __uint_as_float(r[q][4 * e + 1]));
-            const float2 p1 = make_float2(__uint_as_float(r[q][4 * e + 2]), __uint_as_float(r[q][4 * e + 3]));
-            const float2 d0 = fmul2(p0, fadd2(make_float2(__uint_as_float(y[4 * e]),
-                                                          __uint_as_float(y[4 * e + 1])),
-                                              make_float2(nd4.x, nd4.y)));
-            const float2 d1 = fmul2(p1, fadd2(make_float2(__uint_as_float(y[4 * e + 2]),
-                                                          __uint_as_float(y[4 * e + 3])),
-                                              make_float2(nd4.z, nd4.w)));
-            dk[2 * e] = pack_bf16x2(d0.x, d0.y);
-            dk[2 * e + 1] = pack_bf16x2(d1.x, d1.y);
-            if (kDQ) {   // what the rounding leaves
-              pk[2 * e] = rest_bf16x2(d0, dk[2 * e]);
-              pk[2 * e + 1] = rest_bf16x2(d1, dk[2 * e + 1]);
+          for (int h = 0; h < 2; ++h) {   // 16 columns of Y
+            tmem_ld_wait_regs16(y[h]);
+            if (2 * q + h < 7) {
+              tmem_ld16(tY + 16 * (2 * q + h + 1), y[h ^ 1]);
             } else {
-              pk[2 * e] = pack_bf16x2(p0.x, p0.y);
-              pk[2 * e + 1] = pack_bf16x2(p1.x, p1.y);
+              tc_fence_before();
+              mbar_arrive(bar_yf + 8u * (uint32_t)par);
+            }
+            if (left < kChunk) {
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                if (32 * q + 16 * h + u >= left) y[h][u] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float4 nd4 = make_float4(nd_row, nd_row, nd_row, nd_row);
+              if (!kDQ) nd4 = reinterpret_cast<const float4*>(ctl->nd[st])[8 * q + 4 * h + e];
+              const uint32_t* pr = &r[q][16 * h + 4 * e];
+              const float2 p0 = make_float2(__uint_as_float(pr[0]), __uint_as_float(pr[1]));
+              const float2 p1 = make_float2(__uint_as_float(pr[2]), __uint_as_float(pr[3]));
+              const float2 d0 = fmul2(p0, fadd2(make_float2(__uint_as_float(y[h][4 * e]),
+                                                            __uint_as_float(y[h][4 * e + 1])),
+                                                make_float2(nd4.x, nd4.y)));
+              const float2 d1 = fmul2(p1, fadd2(make_float2(__uint_as_float(y[h][4 * e + 2]),
+                                                            __uint_as_float(y[h][4 * e + 3])),
+                                                make_float2(nd4.z, nd4.w)));
+              const int at = 8 * h + 2 * e;
+              dk[at] = pack_bf16x2(d0.x, d0.y);
+              dk[at + 1] = pack_bf16x2(d1.x, d1.y);
+              if (kDQ) {   // what the rounding leaves
+                pk[at] = rest_bf16x2(d0, dk[at]);
+                pk[at + 1] = rest_bf16x2(d1, dk[at + 1]);
+              } else {
+                pk[at] = pack_bf16x2(p0.x, p0.y);
+                pk[at + 1] = pack_bf16x2(p1.x, p1.y);
+              }
             }
           }
           tmem_st16(tX + 16 * q, pk);
