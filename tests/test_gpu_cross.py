@@ -131,6 +131,8 @@ CASES = [
     ([2], [5000], 64, 2, None, None),
     ([3000], [3], 2, 2, None, None),
     ([2000], [1700], 1, 1, None, None),
+    ([600, 300, 129], [700, 50, 400], 16, 16, None, None),   # many items of several costs
+    ([1500], [130], 64, 64, None, None),                     # more equal items than CTAs
 ]
 
 
@@ -162,6 +164,24 @@ def test_forward_and_gradients(nq, nk, heads, kv_heads, qlen, klen, ress_gpu):
         assert torch.equal(a, b)
     only, none = ress_gpu.ress_cross_attn(*dev, want_lse=False, **seqs)
     assert none is None and torch.equal(only, out)
+
+
+def test_pieces_in_two_rounds(ress_gpu):
+    """96 equal items, each cut into three pieces, two pieces per CTA: against
+    float64 on the GPU, and against the same queries in calls of their own."""
+    g = torch.Generator().manual_seed(13)
+    q, k, v = (torch.randn(n, 48, 64, generator=g).to(torch.bfloat16).cuda()
+               for n in (300, 20000, 20000))
+    out, lse = ress_gpu.ress_cross_attn(q, k, v)
+    _ok(ress_gpu)
+    for h in (0, 17, 47):
+        s = q[:, h].double() @ k[:, h].double().T / 8.0
+        want = torch.logsumexp(s, dim=1)
+        p = torch.exp(s - want[:, None])
+        bound = (2.0 ** -8 + 2.0 ** -12) * (p @ v[:, h].double().abs())
+        ref = p @ v[:, h].double()
+        assert ((out[:, h].double() - ref).abs() <= bound + 2.0 ** -8 * ref.abs()).all()
+        assert ((lse[h].double() - want).abs() <= 1e-4 + 1e-5 * want.abs()).all()
 
 
 def test_gradients_against_differences(ress_gpu):
