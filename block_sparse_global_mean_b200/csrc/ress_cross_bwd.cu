@@ -34,6 +34,10 @@
 // delta of the chunk's rows, 4-11 two groups of four warps that take the even
 // and the odd chunks, one row per thread.
 //
+// Bound by the groups' waits for one another's products (a task of 2,500 to 2,850
+// cycles holds 1,024 of tensor work and 1,024 of exponentials) and, at full size,
+// by the power limit, which holds the clock at 1.7 GHz.
+//
 // Both walks are one launch (blockIdx.y), so the second fills the SMs as the
 // first one's CTAs end.
 #define RESS_WAIT_FN __forceinline__
@@ -706,7 +710,7 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
     s.mult = dq ? 1 : g.group;
     s.row_mult = 1;
     s.chunk_log2 = kChunkLog2;
-    s.item_cost = kItemCost;
+    s.item_cost = 5 * kChunk;   // a ragged batch: 165 us at 2 chunks, 151 us at 5
     s.min_share = kMinShare;
     s.grid = kSms;
   }
