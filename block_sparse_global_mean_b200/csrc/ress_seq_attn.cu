@@ -11,8 +11,7 @@
 //          on the tensor core and share each chunk of keys.
 //   split: 128 rows, the two groups take the even and the odd chunks, each with
 //          its own maximum, sum and accumulator; joined in the epilogue.  Used
-//          where a sequence has at most 128 rows, where a second tile would
-//          be empty.
+//          where the second tile of a pair would be empty too often.
 // Either way the tensor core sees one line of tasks i = 0, 1, ...: S of task i
 // in TMEM buffer i % 3, its group i % 2.
 //
@@ -29,6 +28,16 @@
 //
 // Keys outside a row's range get -inf before the maximum; values of such keys
 // are zeroed in shared memory (0 * NaN would reach the sums).
+//
+// Bound by the exponentials at d = 64 (1,024 cycles of MUFU for a chunk of a tile,
+// 512 of tensor work) and by how well the groups' phases overlap: a tile's chunk
+// takes about 1,260 cycles, over the cache 1,520 to 1,800, since the conversion
+// competes for issue slots.  One view against 100 padded ones (16 heads): 1.02 ms,
+// 775 TFLOP/s, 65 % of the exponentials' rate; 9,472 rows against 14,080: 888
+// TFLOP/s.  Measured and left out: S and P in buffers of their own, so that S never
+// waits for P V (one MMA warp 1.14 ms, one per group 1.17 ms against 1.06); 16
+// softmax warps with half a row each (1.16 ms); a quarter or an eighth of the
+// exponentials as polynomials on the FMA pipe (1 % either way, and they hide NaN).
 #define RESS_WAIT_FN __forceinline__
 #include "ress_common.cuh"
 #include "ress_internal.h"
@@ -687,7 +696,15 @@ __global__ void __launch_bounds__(256) seq_combine_kernel(const __grid_constant_
       });
 }
 
-bool use_pair(int nq, int group, int seqs) { return (long long)nq * group > 128ll * seqs; }
+// Pairs share each chunk of keys between two tiles, which makes a tile's chunk
+// 1.18 times as fast (1,024 rows against 40,000 keys, 16 heads: 212 us, split 250
+// us), but pad a sequence to 256 rows (320 rows: 124 us, split 92 us; 192 rows: 71
+// us, split 78 us; 64 rows: 59 us, split 47 us).  So: by the tiles either way of a
+// sequence of the average length.
+bool use_pair(int nq, int group, int seqs) {
+  const long long rows = ((long long)nq * group + seqs - 1) / seqs;
+  return (rows + 255) / 256 * 2 * 100 <= (rows + 127) / 128 * 118;
+}
 
 template <bool kPair, bool kCache>
 ress_status launch_seq_typed(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -719,10 +736,12 @@ size_t parts_bytes(bool pair) {
 size_t cross_workspace(const CrossGeometry& g) {
   return g.nq == 0 ? 0 : parts_bytes(use_pair(g.nq, g.group, g.seqs));
 }
-// Up to 32 rows per request and key head on average, the step that adds a token
-// or a few to every request, go to the register form of ress_cache_decode.cu.
+// Up to 64 rows per request and key head on average, the step that adds a token
+// or a few to every request, go to the register form of ress_cache_decode.cu.  64
+// requests of 2,000 tokens, 4 key heads, both ways: 4 rows 30 and 69 us, 32 rows 40
+// and 73 us, 64 rows 66 and 77 us, 128 rows 115 and 81 us.
 static bool use_decode(int tokens, int group, int requests) {
-  return (long long)tokens * group <= 32ll * requests;
+  return (long long)tokens * group <= 64ll * requests;
 }
 size_t cache_attn_workspace(const ress_cache_shape& s, int heads, int tokens) {
   const int group = heads / s.kv_heads;
