@@ -632,7 +632,7 @@ def _run_on(device: torch.device, stream: Optional[torch.cuda.Stream], fn, *args
     where ``device`` is current already."""
     raw = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
            else stream.cuda_stream)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         return fn(*args, raw)
     with torch.cuda.device(device):
         return fn(*args, raw)
@@ -650,9 +650,10 @@ def _new(shape, dtype: torch.dtype, like: torch.Tensor,
 
 
 def _expect(t: torch.Tensor, shape, dtype: torch.dtype, device: torch.device, name: str) -> int:
-    """``_check_buffer`` and ``_ptr`` in one, for calls that take microseconds."""
-    if (t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_cuda
-            or not t.is_contiguous()):
+    """``_check_buffer`` and ``_ptr`` in one, for calls that take microseconds
+    (``device`` is known to be a CUDA device, or the checks below say so)."""
+    if (t.shape != shape or t.dtype is not dtype or t.device != device
+            or not t.is_contiguous() or device.type != "cuda"):
         _check_buffer(t, shape, dtype, device, name)
         return _ptr(t)
     return t.data_ptr()
