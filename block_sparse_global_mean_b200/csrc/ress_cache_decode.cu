@@ -171,8 +171,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int head1 = seg.head * p.group + rest + 8 - step1 * p.group;
     const size_t row0 = (size_t)(seg.row_start + tok0), row1 = (size_t)(seg.row_start + tok1);
     uint32_t q0[8], q1[8];
-    const float qs0 = load_query(p.q + row0 * p.q_stride + head0 * kHeadDim + 16 * t, live0, q0);
-    const float qs1 = load_query(p.q + row1 * p.q_stride + head1 * kHeadDim + 16 * t, live1, q1);
+    float qs0 = 0.f, qs1 = 0.f;
     const int end0 = live0 ? step_end(seg.cols_valid, seg.rows, tok0, p.step) : seg.cols_valid;
     const int end1 = live1 ? step_end(seg.cols_valid, seg.rows, tok1, p.step) : seg.cols_valid;
     float o[8][4];
@@ -217,6 +216,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       };
 #pragma unroll
       for (int s = 0; s < kStages; ++s) load_next();
+      if (base == seg.c0) {   // behind the first copies, which need two loads before them
+        qs0 = load_query(p.q + row0 * p.q_stride + head0 * kHeadDim + 16 * t, live0, q0);
+        qs1 = load_query(p.q + row1 * p.q_stride + head1 * kHeadDim + 16 * t, live1, q1);
+      }
       while (to_use != 0) {
         const int c = __ffs((int)to_use) - 1;
         to_use &= to_use - 1u;
