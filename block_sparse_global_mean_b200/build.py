@@ -1,4 +1,5 @@
-"""Builds the sm_100a CUDA library ``libress.so`` in-tree with nvcc.
+"""Builds the sm_100a CUDA library ``libress.so`` in-tree with nvcc, and the
+binding's C++ part ``_ress_call.so`` with the host compiler.
 
     python -m block_sparse_global_mean_b200.build
 """
@@ -10,10 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_PATH = os.path.join(PKG_DIR, "libress.so")
+CALL_PATH = os.path.join(PKG_DIR, "_ress_call.so")
+CALL_SOURCE = os.path.join(CSRC, "ress_call.cpp")
+HEADER = os.path.join(PKG_DIR, "..", "include", "ress.h")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -35,17 +40,44 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _older(path: str, deps) -> bool:
+    if not os.path.exists(path):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    deps.append(os.path.join(PKG_DIR, "..", "include", "ress.h"))
+    t = os.path.getmtime(path)
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def needs_build() -> bool:
+    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return _older(LIB_PATH, deps + [HEADER])
+
+
+def build_call(force: bool = False, verbose: bool = False) -> str:
+    """Compile the binding's C++ part against the installed torch; returns its path."""
+    if not force and not _older(CALL_PATH, [CALL_SOURCE, HEADER]):
+        return CALL_PATH
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = CALL_PATH + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{d}" for d in (os.path.join(root, "include"), os.path.join(cuda, "include"),
+                                os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                                sysconfig.get_paths()["include"])),
+           "-o", tmp, CALL_SOURCE, f"-L{os.path.join(root, 'lib')}",
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALL_PATH)
+    return CALL_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every .cu under csrc/ into libress.so (sm_100a); returns its path."""
+    """Compile every .cu under csrc/ into libress.so (sm_100a), and the binding's C++
+    part; returns the library's path."""
+    build_call(force, verbose)
     if not force and not needs_build():
         return LIB_PATH
     tmp = LIB_PATH + ".tmp"

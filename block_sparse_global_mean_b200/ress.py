@@ -605,6 +605,13 @@ def ress_validate_idx(idx: torch.Tensor, n: int, block: int,
 # --------------------------------------------------------------------------------------------
 # Keys of another length, and the 8-bit cache
 # --------------------------------------------------------------------------------------------
+try:   # the common calls in C++ (csrc/ress_call.cpp); without it all of them are made below
+    from . import _ress_call as _call
+    _call.init(LIB_PATH)
+except ImportError:
+    _call = None
+
+
 @functools.lru_cache(maxsize=1024)
 def _cross_shape(nq: int, nk: int, seqs: int, heads: int, kv_heads: int, head_dim: int,
                  q_stride: int, k_stride: int, v_stride: int):
@@ -750,6 +757,10 @@ def ress_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     each that are not padding.  Token rows of q, k and v may be slices of
     wider rows.  Rows of no sequence are left as they were (undefined in a
     tensor that this call allocates).  See include/ress.h."""
+    if _call is not None and out is lse is workspace is stream is None:
+        done = _call.cross_attn(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens, bool(want_lse))
+        if done is not None:
+            return done
     (sh, need, _), qkv, arrays = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
     device, (nq, h, _) = q.device, q.shape
     out, out_ptr, lse, lse_ptr = _attn_outputs(q, out, lse, want_lse, stream)
@@ -789,6 +800,10 @@ def ress_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: 
                         ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients of ress_cross_attn: returns (dq, dk, dv) in the shapes of q,
     k and v, from what the forward call returned and dout [nq, H, 64]."""
+    if _call is not None and dq is dk is dv is workspace is stream is None:
+        done = _call.cross_attn_bwd(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens, out, lse, dout)
+        if done is not None:
+            return done
     (sh, _, need), qkv, arrays = _cross_inputs(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens)
     device, (nq, h, _) = q.device, q.shape
     saved = (_expect(out, q.shape, q.dtype, device, "out"),
@@ -855,6 +870,10 @@ def ress_cache_plan(added: torch.Tensor, lengths: torch.Tensor, table: torch.Ten
     new_lengths [R], new_cursor [1]), all int32 (parts of one allocation unless
     any is passed in).  ``tokens`` is the length of the slot map (at least the sum of ``added``); ``pages`` bounds the page ids
     (default: the largest pool).  See include/ress.h."""
+    if _call is not None and offsets is slots is new_lengths is new_cursor is stream is None:
+        done = _call.cache_plan(added, lengths, table, free_pages, cursor, page, tokens, pages)
+        if done is not None:
+            return done
     device, i32 = added.device, torch.int32
     if added.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("added must be [R], table [R, max_pages], free_pages [n]")
@@ -886,6 +905,8 @@ def ress_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cac
     """Writes the tokens k, v [tokens, Hk, 64] (bf16 or float32; rows may be
     slices of wider ones) into the cells ``slots`` [tokens] int32 of ``cache``,
     in place; negative slots skip their token.  See include/ress.h."""
+    if _call is not None and stream is None and _call.cache_append(k, v, slots, *cache):
+        return
     device = k.device
     (pages, page, heads, d), parts = _check_cache(cache, device)
     _check_rows(k, "k", device, heads, (torch.bfloat16, torch.float32))
@@ -915,6 +936,10 @@ def ress_cache_attn(q: torch.Tensor, cache: ress_cache, table: torch.Tensor,
     max_pages] names their pages.  ``step`` 0: every query sees all of its
     request; 1: causal; n: groups of n tokens see themselves and the earlier
     groups.  See include/ress.h."""
+    if _call is not None and out is lse is workspace is stream is None:
+        done = _call.cache_attn(q, *cache, table, lengths, offsets, step, bool(want_lse))
+        if done is not None:
+            return done
     device, i32 = q.device, torch.int32
     (pages, page, heads, d), parts = _check_cache(cache, device)
     _check_rows(q, "q", device)

@@ -184,6 +184,35 @@ def test_pieces_in_two_rounds(ress_gpu):
         assert ((lse[h].double() - want).abs() <= 1e-4 + 1e-5 * want.abs()).all()
 
 
+def test_compiled_and_python_calls_agree(ress_gpu):
+    """The binding's C++ part and the Python code behind it make the same call, and
+    raise the same errors."""
+    q, k, v, do = (t.cuda() for t in make([50, 7], [90, 33], 4, 2, seed=21))
+    seqs = dict(q_offsets=_off([50, 7]), kv_offsets=_off([90, 33]), kv_lens=_i32([80, 33]))
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    call = ress_gpu._call
+    assert call is not None
+    fast = call.cross_attn(q, k, v, seqs["q_offsets"], seqs["kv_offsets"], None, seqs["kv_lens"], True)
+    slow = ress_gpu.ress_cross_attn(q, k, v, **seqs, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(fast, slow))
+    args = (q, k, v, seqs["q_offsets"], seqs["kv_offsets"], None, seqs["kv_lens"])
+    fast = call.cross_attn_bwd(*args, *slow, do)
+    slow = ress_gpu.ress_cross_attn_bwd(q, k, v, *slow, do, **seqs, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(fast, slow))
+    _ok(ress_gpu)
+    with pytest.raises(TypeError, match="kv_lens must be"):
+        ress_gpu.ress_cross_attn(q, k, v, kv_lens=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="kv_offsets must have shape"):
+        ress_gpu.ress_cross_attn(q, k, v, q_offsets=_off([50, 7]), kv_offsets=_off([90]))
+    with pytest.raises(TypeError, match="k must be"):
+        ress_gpu.ress_cross_attn(q, k.float(), v.float())
+    with pytest.raises(ValueError, match="must be on"):
+        ress_gpu.ress_cross_attn(q, k, v, kv_lens=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ress_gpu.RessError):
+        ress_gpu.ress_cross_attn(q, k[:, :1].expand(-1, 3, -1).contiguous(),
+                                 k[:, :1].expand(-1, 3, -1).contiguous())     # 3 does not divide 4
+
+
 def test_gradients_against_differences(ress_gpu):
     """The directional derivative of sum(out * dout) along random directions of
     q, k and v: central differences of the float64 forward, whose own error is

@@ -235,3 +235,22 @@ def test_binding_refuses_mismatched_tensors(ress):
         ress.ress_cache_plan(off, off[:2], table, off, off[:1], 64, 9)
     with pytest.raises(ValueError, match="cursor must have shape"):
         ress.ress_cache_plan(off, off, table, off, off, 64, 9)
+
+
+def test_compiled_calls_leave_to_python_what_is_not_common(ress):
+    """The C++ part of the binding takes CUDA tensors of the right kind alone, and
+    says None to everything else, whatever it is given."""
+    assert ress._call is not None
+    q, k = torch.zeros(10, 4, 64, dtype=torch.bfloat16), torch.zeros(20, 2, 64, dtype=torch.bfloat16)
+    cache = ress.make_cache(4, 2, 64, device="cpu")
+    i32 = torch.zeros(3, dtype=torch.int32)
+    for f, args in ((ress._call.cross_attn, (q, k, k, None, None, None, None, True)),
+                    (ress._call.cross_attn_bwd, (q, k, k, None, None, None, None, q, q, q)),
+                    (ress._call.cache_plan, (i32, i32, i32[:, None], i32, i32[:1], 64, 5, None)),
+                    (ress._call.cache_append, (k, k, i32, *cache)),
+                    (ress._call.cache_attn, (q, *cache, i32[:, None], i32, i32, 0, True))):
+        assert f(*args) is None
+        assert f() is None and f(*args[:-1]) is None and f(*args, 1) is None
+        for i in range(len(args)):
+            for x in (None, 3, -1, 2 ** 70, "x", q.numpy if i % 2 else [q]):
+                assert f(*args[:i], x, *args[i + 1:]) is None
