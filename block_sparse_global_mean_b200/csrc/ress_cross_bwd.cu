@@ -713,6 +713,7 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
     s.item_cost = 5 * kChunk;   // a ragged batch: 165 us at 2 chunks, 151 us at 5
     s.min_share = kMinShare;
     s.grid = kSms;
+    sched_plan_on_host(&s);
   }
   CUtensorMap tq, tdo, tqg, tdog, tk, tv;
   const int64_t dense = (int64_t)g.heads * kHeadDim;

@@ -53,6 +53,7 @@ struct SchedParams {
   int chunk_log2;             // columns per chunk
   int item_cost, min_share;   // units
   int grid;                   // workers
+  int items, ns;              // ns > 0: the host knew the lengths and planned rounds
   long long max_len;          // largest valid entry of `lengths`
 };
 
@@ -154,6 +155,12 @@ __device__ __forceinline__ long long sched_even(long long total, int parts) {
 // The plan, and where `worker` begins (at == ub: nowhere).  Called by a warp.
 __device__ __forceinline__ SchedPlan sched_begin(const SchedParams& p, int worker, SchedWalk* walk) {
   const int lane = threadIdx.x & 31;
+  walk->worker = worker;
+  if (p.ns > 0) {
+    walk->at = worker;
+    walk->ub = (long long)p.items * p.ns;
+    return SchedPlan{kRounds, 0, p.items, p.ns};
+  }
   const bool few = p.seqs <= 32;   // a sequence per lane: its cost stays in registers
   SeqCost cost{0, 0, 0};
   long long units = 0;
@@ -166,7 +173,6 @@ __device__ __forceinline__ SchedPlan sched_begin(const SchedParams& p, int worke
   const bool none = items == 0;
   units = warp_sum(units);
   items = __reduce_add_sync(0xffffffffu, items);
-  walk->worker = worker;
   walk->at = walk->ub = 0;
   SchedPlan plan{kLine, max(sched_even(units, p.grid), (long long)p.min_share), items, 1};
   if (items == 0) return plan;
@@ -240,6 +246,35 @@ __device__ __forceinline__ SchedPlan sched_begin(const SchedParams& p, int worke
   return plan;
 }
 
+// The same choice on the host, where one sequence of known length needs none on the
+// device (five queries against 1374 states: 14.0 -> 11.8 us).
+inline void sched_plan_on_host(SchedParams* p) {
+  p->items = p->ns = 0;
+  if (p->row_off || p->col_off || p->col_lens || p->lengths || p->step || p->seqs != 1) return;
+  const long long chunk = 1ll << p->chunk_log2;
+  const long long chunks = (p->cols + chunk - 1) / chunk * p->mult;
+  const long long items =
+      ((long long)p->rows * p->row_mult + p->tile_rows - 1) / p->tile_rows * p->heads;
+  if (items == 0 || items >= (1 << 20)) return;
+  const long long fixed = (p->item_cost + chunk - 1) / chunk;
+  const long long units = items * (p->item_cost + chunks * chunk);
+  long long best = 1ll << 60, share = (units + p->grid - 1) / p->grid;
+  int best_ns = 1;
+  for (int i = 0; i < 32; ++i) {
+    long long ns = i < 30 ? i + 1 : (i - 29) * (long long)p->grid / items;
+    ns = ns > chunks ? chunks : ns;
+    ns = ns < 1 ? 1 : ns;
+    const long long rounds = (items * ns + p->grid - 1) / p->grid;
+    if (ns > 1 && rounds > 2) continue;
+    const long long t = rounds * (fixed + (chunks + ns - 1) / ns);
+    if (t < best || (t == best && ns < best_ns)) best = t, best_ns = (int)ns;
+  }
+  share = share < p->min_share ? p->min_share : share;
+  if (best * chunk > share + (share >> 4) + p->item_cost) return;
+  p->items = (int)items;
+  p->ns = best_ns;
+}
+
 // The item at a unit of a sequence on the line.
 struct SchedItem {
   int head, tile;
@@ -310,11 +345,13 @@ __device__ __forceinline__ Segment sched_next(const SchedParams& p, const SchedP
     g.slot = w.at >= p.grid ? 1 : 0;   // of whole items, where there may be more rounds, unused
     g.stride = plan.items;
     w.at += p.grid;
-    for (w.b = 0;; ++w.b) {
-      const int n = sched_cost(p, w.b).tiles * p.heads;
-      if (item < n) break;
-      item -= n;
-    }
+    w.b = 0;
+    if (p.seqs > 1)
+      for (;; ++w.b) {
+        const int n = sched_cost(p, w.b).tiles * p.heads;
+        if (item < n) break;
+        item -= n;
+      }
   }
   for (;;) {
     const SeqRange r = sched_rows(p, w.b), c = sched_cols(p, w.b);

@@ -713,6 +713,7 @@ ress_status launch_seq_typed(const CUtensorMap& tq, const CUtensorMap& tk, const
   constexpr size_t smem = 1024 + C::q_bytes + C::stages * kStageBytes + sizeof(Ctl);
   static_assert(smem <= 227 * 1024, "shared memory");
   p.sched.tile_rows = p.tps * (kPair ? 2 : 1);
+  sched_plan_on_host(&p.sched);
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)kSms * 2 * C::rows * kHeadDim);
   p.split = reinterpret_cast<SplitItem*>(p.part_ml + (size_t)kSms * 2 * C::rows);
