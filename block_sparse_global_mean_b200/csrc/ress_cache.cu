@@ -65,6 +65,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
   __shared__ int s_taken;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool lead = blockIdx.x == 0;
+  wait_for_previous_kernel();
   const int cursor = p.cursor[0];
   const bool cursor_ok = cursor >= 0 && cursor <= p.n_free;
   if (threadIdx.x == 0) s_taken = 0;
@@ -205,7 +206,7 @@ template <>
 struct Eight<__nv_bfloat16> {
   uint4 w;
   __device__ __forceinline__ void load(const __nv_bfloat16* src) {
-    w = __ldg(reinterpret_cast<const uint4*>(src));
+    w = *reinterpret_cast<const uint4*>(src);
   }
   __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
   // Largest magnitudes so far, as the bits of two bf16.
@@ -231,8 +232,8 @@ template <>
 struct Eight<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* src) {
-    a = __ldg(reinterpret_cast<const float4*>(src));
-    b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+    a = *reinterpret_cast<const float4*>(src);
+    b = *(reinterpret_cast<const float4*>(src) + 1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   // Largest magnitude so far, as bits.
@@ -270,13 +271,14 @@ __global__ void __launch_bounds__(kPage, (sizeof(T) == 2 ? 1152 : 704) / kPage)
   const int head = (int)((blockIdx.x >> 1) % (unsigned)p.kv_heads);
   const long long t0 = (long long)((blockIdx.x >> 1) / (unsigned)p.kv_heads) * window;
   constexpr int mask = kPage - 1;
+  wait_for_previous_kernel();
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const long long pos = t0 + u * kPage + threadIdx.x;
     bool cont = false, start = false;
     if (pos < p.tokens) {
-      const int s = __ldg(p.slots + pos);
-      const int prev = pos > 0 ? __ldg(p.slots + pos - 1) : -1;
+      const int s = p.slots[pos];
+      const int prev = pos > 0 ? p.slots[pos - 1] : -1;
       cont = s >= 0 && prev >= 0 && prev + 1 == s && (s & mask) != 0;
       start = u == 0 && s >= 0 && !cont && (int)threadIdx.x < window;
     }
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kPage, (sizeof(T) == 2 ? 1152 : 704) / kPage)
     for (uint32_t todo = s_start[word]; todo != 0; todo &= todo - 1u) {
       const int bit = word * 32 + __ffs((int)todo) - 1;
       const long long first = t0 + bit;
-      const int slot = __ldg(p.slots + first);
+      const int slot = p.slots[first];
       const int page = slot / kPage, c = slot & mask;
       if (page >= p.pages) {
         if (threadIdx.x == 0) raise_device_error(p.err, RESS_ERR_BAD_INDEX, 104);
@@ -376,15 +378,16 @@ __global__ void __launch_bounds__(kPage, (sizeof(T) == 2 ? 1152 : 704) / kPage)
 }
 
 template <typename T>
-void launch_append_typed(const AppendParams& p, cudaStream_t st) {
+cudaError_t launch_append_typed(const AppendParams& p, cudaStream_t st) {
   // Runs that start in one window are written one after another.  Whole views
   // start one run per page of tokens, so a window is a page; short calls (a few
   // tokens each for many requests) start one per token or few (64 requests of one
   // token: 3.7 us; in one window their 64 runs would follow one another).
   const int window = p.tokens <= 1024 ? 1 : p.tokens <= 4096 ? 8 : p.page;
   const unsigned blocks = (unsigned)(((long long)p.tokens + window - 1) / window * p.kv_heads * 2);
-  if (p.page == 64) cache_append_kernel<T, 64><<<blocks, 64, 0, st>>>(p, window);
-  else cache_append_kernel<T, 128><<<blocks, 128, 0, st>>>(p, window);
+  return p.page == 64
+             ? launch_behind(cache_append_kernel<T, 64>, dim3(blocks), dim3(64), 0, st, p, window)
+             : launch_behind(cache_append_kernel<T, 128>, dim3(blocks), dim3(128), 0, st, p, window);
 }
 
 }  // namespace
@@ -420,9 +423,9 @@ ress_status launch_cache_plan(const ress_cache_shape& s, const int32_t* added,
       return e;
   const long long items = (long long)tokens + s.requests;
   const long long blocks = (items + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-  cache_plan_kernel<<<(unsigned)(blocks < 1 ? 1 : blocks > 148 ? 148 : blocks), kPlanThreads, smem,
-                      st>>>(p);
-  return record_cuda(cudaGetLastError());
+  return record_cuda(launch_behind(cache_plan_kernel,
+                                   dim3((unsigned)(blocks < 1 ? 1 : blocks > 148 ? 148 : blocks)),
+                                   dim3(kPlanThreads), smem, st, p));
 }
 
 ress_status launch_cache_append(const ress_cache_shape& s, const void* k, const void* v, bool f32,
@@ -445,9 +448,8 @@ ress_status launch_cache_append(const ress_cache_shape& s, const void* k, const 
   p.kv_heads = s.kv_heads;
   p.page = s.page;
   p.pages = s.pages;
-  if (f32) launch_append_typed<float>(p, st);
-  else launch_append_typed<__nv_bfloat16>(p, st);
-  return record_cuda(cudaGetLastError());
+  return record_cuda(f32 ? launch_append_typed<float>(p, st)
+                         : launch_append_typed<__nv_bfloat16>(p, st));
 }
 
 }  // namespace ress

@@ -103,12 +103,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // 16 values of a query row as f16 times 2^(14 - e), e the exponent of the row's
 // largest; returns 2^(e - 14).  The four threads of a row agree by shuffles.
-__device__ __forceinline__ float load_query(const __nv_bfloat16* src, bool live, uint32_t (&w)[8]) {
-  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-  if (live) {
-    a = __ldg(reinterpret_cast<const uint4*>(src));
-    b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-  }
+__device__ __forceinline__ float query_f16(uint4 a, uint4 b, uint32_t (&w)[8]) {
   const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   uint32_t top = 0;
 #pragma unroll
@@ -136,6 +131,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     fence_mbarrier_init();
   }
   if (threadIdx.x == 0) sm->abort_flag = 0;
+  wait_for_previous_kernel();
   allow_next_kernel();
   __syncthreads();
   const int worker = warp * kSms + (int)blockIdx.x;   // few workers: spread over the SMs
@@ -185,13 +181,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       int id = -1;
       float ks = 0.f, vs = 0.f;
       if (lane < n) {
-        id = __ldg(p.table + (size_t)seg.b * p.max_pages + (((base + lane) * kKeys) >> p.page_log2));
+        id = p.table[(size_t)seg.b * p.max_pages + (((base + lane) * kKeys) >> p.page_log2)];
         if (id < 0 || id >= p.pages) {
           raise_device_error(p.err, RESS_ERR_BAD_INDEX, 95);
           id = -1;
         } else {
-          ks = __ldg(p.k_scale + (size_t)id * p.kv_heads + seg.head);
-          vs = __ldg(p.v_scale + (size_t)id * p.kv_heads + seg.head);
+          ks = p.k_scale[(size_t)id * p.kv_heads + seg.head];
+          vs = p.v_scale[(size_t)id * p.kv_heads + seg.head];
         }
       }
       // Chunks of the pool; the others are left out.
@@ -217,8 +213,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
       for (int s = 0; s < kStages; ++s) load_next();
       if (base == seg.c0) {   // behind the first copies, which need two loads before them
-        qs0 = load_query(p.q + row0 * p.q_stride + head0 * kHeadDim + 16 * t, live0, q0);
-        qs1 = load_query(p.q + row1 * p.q_stride + head1 * kHeadDim + 16 * t, live1, q1);
+        const __nv_bfloat16* src0 = p.q + row0 * p.q_stride + head0 * kHeadDim + 16 * t;
+        const __nv_bfloat16* src1 = p.q + row1 * p.q_stride + head1 * kHeadDim + 16 * t;
+        uint4 a0 = make_uint4(0u, 0u, 0u, 0u), b0 = a0, a1 = a0, b1 = a0;
+        if (live0) {
+          a0 = reinterpret_cast<const uint4*>(src0)[0];
+          b0 = reinterpret_cast<const uint4*>(src0)[1];
+        }
+        if (live1) {
+          a1 = reinterpret_cast<const uint4*>(src1)[0];
+          b1 = reinterpret_cast<const uint4*>(src1)[1];
+        }
+        qs0 = query_f16(a0, b0, q0);
+        qs1 = query_f16(a1, b1, q1);
       }
       while (to_use != 0) {
         const int c = __ffs((int)to_use) - 1;
@@ -408,6 +415,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 __global__ void __launch_bounds__(256)
     cache_decode_combine_kernel(const __grid_constant__ DecodeParams p) {
   wait_for_previous_kernel();
+  allow_next_kernel();
   const SplitItem it = load_split(p.split + blockIdx.x);
   if (it.head < 0) return;
   auto token_of = [&](int r) { return (size_t)(it.row_start + (it.tile * kRows + r) / p.group); };
@@ -472,8 +480,9 @@ ress_status launch_cache_decode(const CrossParams& c, void* ws, cudaStream_t st)
   if (ress_status s =
           allow_smem(reinterpret_cast<const void*>(cache_decode_kernel), kSmem, &allowed))
     return s;
-  cache_decode_kernel<<<kSms, kWarps * 32, kSmem, st>>>(p);
-  if (ress_status s = record_cuda(cudaGetLastError())) return s;
+  if (ress_status s = record_cuda(
+          launch_behind(cache_decode_kernel, dim3(kSms), dim3(kWarps * 32), kSmem, st, p)))
+    return s;
   return record_cuda(
       launch_dependent(cache_decode_combine_kernel, dim3(kWorkers), dim3(256), st, p));
 }

@@ -101,16 +101,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // lanes per row, 16 bytes each.  A row without a key (lse -inf) gets
 // nl = -inf, which makes its P zero.  Bound by reading out and dout once.
 __global__ void __launch_bounds__(256)
-    cross_delta_kernel(const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
-                       const float* __restrict__ lse, float* __restrict__ nl,
-                       float* __restrict__ nd, int nq, int heads) {
+    cross_delta_kernel(const __nv_bfloat16* out, const __nv_bfloat16* dout, const float* lse,
+                       float* nl, float* nd, int nq, int heads) {
   const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) >> 3;
   const long long rows = (long long)nq * heads;
   const int sub = threadIdx.x & 7;
   float d = 0.f;
+  wait_for_previous_kernel();
   if (at < rows) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(out + at * kHeadDim) + sub);
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(dout + at * kHeadDim) + sub);
+    const uint4 a = *(reinterpret_cast<const uint4*>(out + at * kHeadDim) + sub);
+    const uint4 b = *(reinterpret_cast<const uint4*>(dout + at * kHeadDim) + sub);
     const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -381,8 +381,8 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
               const int i = col + lane + 32 * u;
               const bool in = i < g.cols_valid;
               const size_t at = (size_t)head * p.nq + g.col_start + i;
-              a[u] = in ? __ldg(p.nl + at) : -INFINITY;
-              b[u] = in ? __ldg(p.nd + at) : 0.f;
+              a[u] = in ? p.nl[at] : -INFINITY;
+              b[u] = in ? p.nd[at] : 0.f;
             }
             if (kc >= kStages &&
                 !warp_wait(bar_be + 8 * st, ((kc / kStages) - 1) & 1, abortf, p.err, 153))
@@ -426,8 +426,8 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
       const int head = kDQ ? g.head * p.group + head_in_group : g.head;
       float nl_row = -INFINITY, nd_row = 0.f;
       if (kDQ && real) {
-        nl_row = __ldg(p.nl + (size_t)head * p.nq + row);
-        nd_row = __ldg(p.nd + (size_t)head * p.nq + row);
+        nl_row = p.nl[(size_t)head * p.nq + row];
+        nd_row = p.nd[(size_t)head * p.nq + row];
       }
       bool ok = true;
       for (int i = par; i < n; i += 2, ++cnt) {
@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(256)
   const SchedParams& sp = p.sched[dq ? 1 : 0];
   const int first = (int)blockIdx.x;
   wait_for_previous_kernel();
+  allow_next_kernel();
   const SplitItem it = load_split(p.split + (dq ? kSms : 0) + first);
   if (it.head < 0) return;
   const int lane = threadIdx.x & 31;
@@ -724,9 +725,10 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
         !make_rows_map(&tdog, c.dout, g.heads, g.nq, dense, g.group, p.tps))
       return RESS_ERR_CUDA;
     const long long threads = (long long)g.nq * g.heads * 8;
-    cross_delta_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(
-        c.out, c.dout, c.lse, nl, nd, g.nq, g.heads);
-    if (ress_status e = record_cuda(cudaGetLastError())) return e;
+    if (ress_status e = record_cuda(
+            launch_behind(cross_delta_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0,
+                          st, c.out, c.dout, c.lse, nl, nd, g.nq, g.heads)))
+      return e;
   }
   if (g.nk > 0 && (!make_rows_map(&tk, c.k, g.kv_heads, g.nk, g.k_stride, 1, 128) ||
                    !make_rows_map(&tv, c.v, g.kv_heads, g.nk, g.v_stride, 1, 128)))
@@ -751,6 +753,7 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
   if (ress_status e = record_cuda(
           cudaLaunchKernelEx(&cfg, cross_bwd_kernel, tq, tdo, tqg, tdog, tk, tv, p)))
     return e;
+  if (p.sched[0].ns == 1 && p.sched[1].ns == 1) return RESS_OK;   // no item is cut
   return record_cuda(launch_dependent(cross_bwd_combine_kernel, dim3(kSms, 2, 4), dim3(256), st, p));
 }
 

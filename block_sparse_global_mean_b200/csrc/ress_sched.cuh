@@ -526,28 +526,4 @@ __device__ __forceinline__ void join_item(const SplitItem& it, int first, int gr
   }
 }
 
-// Programmatic dependent launch: the second kernel of an operator is launched
-// while the first still runs, plans its work, and waits here for the first
-// one's results.
-__device__ __forceinline__ void wait_for_previous_kernel() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-__device__ __forceinline__ void allow_next_kernel() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-template <typename Kernel, typename... Args>
-cudaError_t launch_dependent(Kernel kernel, dim3 grid, dim3 block, cudaStream_t st, Args... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace ress

@@ -222,6 +222,7 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
       tma_prefetch_desc(&tm_v);
     }
   }
+  wait_for_previous_kernel();
   allow_next_kernel();
   SchedWalk walk{0, 0, 0, 0, 0};
   SchedPlan plan;
@@ -618,14 +619,14 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
         if (have) {
           const size_t ph = (size_t)id * p.kv_heads + hk;
           const size_t off = ((ph << p.page_log2) + (size_t)(at & mask)) * kHeadDim;
-          ks = __ldg(p.k_scale + ph);
-          vs = __ldg(p.v_scale + ph);
+          ks = p.k_scale[ph];
+          vs = p.v_scale[ph];
           const uint4* ksrc = reinterpret_cast<const uint4*>(p.k_cache + off);
           const uint4* vsrc = reinterpret_cast<const uint4*>(p.v_cache + off);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            kw[u] = __ldg(ksrc + u);
-            vw[u] = __ldg(vsrc + u);
+            kw[u] = ksrc[u];
+            vw[u] = vsrc[u];
           }
         } else {
 #pragma unroll
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
           ks = vs = 0.f;
         }
       };
-      auto page_of = [&](int at) { return at < cols ? __ldg(tab + (at >> p.page_log2)) : -1; };
+      auto page_of = [&](int at) { return at < cols ? tab[at >> p.page_log2] : -1; };
       int id_next = n > 1 ? page_of(pos + kChunk) : -1;
       if (n > 0) fetch(page_of(pos), pos);
       for (int c = 0; c < n; ++c, ++kc, pos += kChunk) {
@@ -676,6 +677,7 @@ template <bool kPair>
 __global__ void __launch_bounds__(256) seq_combine_kernel(const __grid_constant__ SeqAttnParams p) {
   constexpr int kRows = kPair ? 256 : 128;
   wait_for_previous_kernel();
+  allow_next_kernel();
   const SplitItem it = load_split(p.split + blockIdx.x);
   if (it.head < 0) return;
   auto token_of = [&](int r) { return it.tile * p.sched.tile_rows + (r >> 7) * p.tps + (r & 127) / p.group; };
@@ -721,8 +723,10 @@ ress_status launch_seq_typed(const CUtensorMap& tq, const CUtensorMap& tk, const
   if (ress_status s =
           allow_smem(reinterpret_cast<const void*>(seq_attn_kernel<kPair, kCache>), smem, &allowed))
     return s;
-  seq_attn_kernel<kPair, kCache><<<kSms, C::threads, smem, st>>>(tq, tk, tv, p);
-  if (ress_status s = record_cuda(cudaGetLastError())) return s;
+  if (ress_status s = record_cuda(launch_behind(seq_attn_kernel<kPair, kCache>, dim3(kSms),
+                                                dim3(C::threads), smem, st, tq, tk, tv, p)))
+    return s;
+  if (p.sched.ns == 1) return RESS_OK;   // no item is cut
   return record_cuda(launch_dependent(seq_combine_kernel<kPair>, dim3(kSms, C::rows / 32),
                                       dim3(256), st, p));
 }

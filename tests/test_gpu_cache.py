@@ -635,3 +635,60 @@ def test_calls_on_another_stream_and_two_at_once(queries, ress_gpu):
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
     _ok(ress_gpu)
+
+
+@pytest.mark.parametrize("new", [1, 150])
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_calls_in_a_row_wait_for_one_another(new, own_stream, ress_gpu):
+    """Kernels start while the one before them ends.  Chains of calls, each on the
+    outputs of the last, with buffers that are written over behind the calls that
+    read them: queued behind a busy GPU they give the very bits that they give
+    with a wait after each call."""
+    page, heads, kv_heads, r, pool, steps = 64, 4, 2, 2, 40, 8
+    g = torch.Generator().manual_seed(3)
+    free = torch.randperm(pool, generator=g).to(torch.int32).cuda()
+    first = torch.randn(r * new, 2 * heads, 64, generator=g).to(torch.bfloat16).cuda()
+    noise = torch.randn(steps, r * new, heads, 64, generator=g).to(torch.bfloat16).cuda()
+    added, total = _i32([new] * r), r * new
+
+    def chain(wait):
+        pause = torch.cuda.synchronize if wait else lambda: None
+        cache = ress_gpu.make_cache(pool, kv_heads, page)
+        table = torch.full((r, 20), -1, dtype=torch.int32, device="cuda")
+        lengths, cursor = _i32([0] * r), _i32([0])
+        x, got = first.clone(), []
+        pause()
+        if not wait:
+            torch.cuda._sleep(20_000_000)
+        for s in range(steps):
+            off, slots, new_len, new_cur = ress_gpu.ress_cache_plan(
+                added, lengths, table, free, cursor, page, total, pages=pool)
+            pause()
+            lengths.copy_(new_len)
+            cursor.copy_(new_cur)
+            q, k, v = x[:, :heads], x[:, heads:heads + kv_heads], x[:, heads + kv_heads:]
+            ress_gpu.ress_cache_append(k, v, slots, cache)
+            pause()
+            out, lse = ress_gpu.ress_cache_attn(q, cache, table, new_len, off)
+            pause()
+            two, lse2 = ress_gpu.ress_cross_attn(out, k, v, off, off)
+            pause()
+            grads = ress_gpu.ress_cross_attn_bwd(out, k, v, two, lse2, out, off, off)
+            pause()
+            x[:, :heads] = two + noise[s]
+            x[:, heads:heads + kv_heads] = grads[1].clamp(-4, 4)   # unbounded, the chain
+            x[:, heads + kv_heads:] = grads[2].clamp(-4, 4)        # itself grows to infinity
+            got += [off, slots, new_len, out.clone(), lse, two, lse2, *grads]
+            out.zero_()
+            pause()
+        return got + list(cache) + [table]
+
+    stream = torch.cuda.Stream() if own_stream else torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        want = chain(True)
+        runs = [chain(False) for _ in range(3)]
+        torch.cuda.synchronize()
+    _ok(ress_gpu)
+    for got in runs:
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
