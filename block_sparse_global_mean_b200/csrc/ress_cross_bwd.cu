@@ -182,14 +182,14 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
     tma_prefetch_desc(tm_b1);
     tma_prefetch_desc(tm_b2);
   }
+  wait_for_previous_kernel();   // delta, and what came before it
+  allow_next_kernel();
   SchedWalk walk{0, 0, 0, 0, 0};
   SchedPlan plan;
   if (warp == 2) {
     plan = sched_begin(sp, (int)blockIdx.x, &walk);
     if (lane == 0) ctl->seg[0] = sched_next(sp, plan, walk);
   }
-  wait_for_previous_kernel();   // delta
-  allow_next_kernel();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
