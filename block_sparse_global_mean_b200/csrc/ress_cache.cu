@@ -180,11 +180,14 @@ struct AppendParams {
 
 // Exponent e of the smallest power of two with amax <= 448 * 2^e, at least
 // -100: 448 = 1.75 * 2^8, so the mantissa of amax decides between two values.
+// At most 119: a code up to 256 stands in a page of scale 2^120, which would be
+// an infinity.
 __device__ __forceinline__ int scale_exponent(float amax) {
   const uint32_t bits = __float_as_uint(amax);
   const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return max(e, -100);
+  return min(max(e, -100), 119);
 }
+constexpr uint32_t kMostBits = 0x7f600000u;   // 448 * 2^119: what a cell can hold
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // Two float32 values as e4m3 codes (nearest, ties to even, saturating); a is the low byte.
@@ -323,12 +326,13 @@ __global__ void __launch_bounds__(kPage, (sizeof(T) == 2 ? 1152 : 704) / kPage)
         else v[k].zero();
       }
       // Largest magnitude as bits, which order as the values do, with infinities
-      // and NaN on top; the scale is that of the finite ones.
+      // and NaN on top; the scale is that of the finite ones.  What no cell can
+      // hold is flagged: those two, and values beyond 448 * 2^119.
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = v[k].most(top);
       top = __reduce_max_sync(0xffffffffu, Eight<T>::bits(top));
-      if (top >= 0x7f800000u) {
+      if (top > kMostBits) {
         if (lane == 0) raise_device_error(p.err, RESS_ERR_INVALID_ARG, 105);
         top = 0;
 #pragma unroll

@@ -597,7 +597,7 @@ ress_status ress_cache_plan(const ress_cache_shape* shape, const int32_t* added,
  * Slots of one page must stand together and ascend by one (as
  * ress_cache_plan writes them): a run.  For each run, head and tensor, with c
  * the run's first cell and amax the largest |x| of its tokens,
- *   s = smallest power of two >= 2^-100 with amax <= 448 s,
+ *   s = smallest power of two >= 2^-100 with amax <= 448 s, at most 2^119,
  *   s = max(s, old scale) when c > 0;
  * the page's scale becomes s, the run's codes are x / s rounded to e4m3
  * (nearest, ties to even), and when c > 0 the codes of cells 0 .. c - 1 are
@@ -606,9 +606,10 @@ ress_status ress_cache_plan(const ress_cache_shape* shape, const int32_t* added,
  *
  *   A page that appears in two runs of one call gets an undefined content
  *   (two runs write it at once); slots outside the pool are skipped and
- *   flagged (RESS_ERR_BAD_INDEX, detail 104).  Values must be finite: one that
- *   is not is flagged (RESS_ERR_INVALID_ARG, detail 105) and does not count for
- *   the scale; its code is NaN, or for an infinity the largest number.
+ *   flagged (RESS_ERR_BAD_INDEX, detail 104).  Values must be at most 448 * 2^119
+ *   (2.98e38) in magnitude: one that is not is flagged (RESS_ERR_INVALID_ARG,
+ *   detail 105).  Its code is the largest number, or NaN for NaN; infinities and
+ *   NaN do not count for the scale.
  *   shape->requests and max_pages are not used.  One launch, no workspace.
  */
 ress_status ress_cache_append(const ress_cache_shape* shape, const void* k, const void* v,

@@ -1,0 +1,70 @@
+"""Edges of the paged 8-bit cache on the GPU: the largest numbers it can hold and
+what lies beyond them."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.parity import np64
+
+pytestmark = pytest.mark.gpu
+
+FP8 = torch.float8_e4m3fn
+
+
+def _i32(v, device="cuda"):
+    return torch.tensor(v, dtype=torch.int32, device=device)
+
+
+def _ok(ress):
+    status, detail = ress.ress_check_device_errors()
+    assert status == 0, (status, detail)
+
+
+# ------------------------------------------------------------------------------------------
+# the largest numbers
+# ------------------------------------------------------------------------------------------
+MOST = 448.0 * 2.0 ** 119
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("big,flagged", [(MOST, False), (3.3e38, True), (-3.3895e38, True)])
+def test_append_of_the_largest_numbers(big, flagged, dtype, ress_gpu):
+    """448 * 2^119 is what a cell holds at most: larger values are flagged, stand as
+    that number and raise the scale to 2^119 and no further."""
+    x = torch.full((3, 1, 64), 2.0 ** 118, dtype=dtype)
+    x[1, 0, 5] = big
+    cache = ress_gpu.make_cache(1, 1, 64)
+    ress_gpu.ress_cache_append(x.cuda(), x.cuda(), _i32([0, 1, 2]), cache)
+    status, detail = ress_gpu.ress_check_device_errors()
+    assert (status, detail) == ((ress_gpu.RESS_ERR_INVALID_ARG, 105) if flagged else (0, 0))
+    want = np64(x)[:, 0]
+    want[1, 5] = math.copysign(MOST, big)
+    for codes, scale in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+        assert np64(scale)[0, 0] == 2.0 ** 119
+        assert np.array_equal(np64(codes)[0, 0, :3] * 2.0 ** 119, want)
+
+
+@pytest.mark.parametrize("queries", [1, 70])
+def test_attention_over_the_largest_numbers(queries, ress_gpu):
+    """Values near the largest float come back finite from both kernels.  Codes and
+    the probabilities 1/2 are exact here, so outputs differ by their rounding alone
+    (half a step, 2^-8), and the keys' logits of 0 make lse = ln 2.  (The float32
+    sums before the division stay below 3.4e38 as well.)"""
+    x = torch.full((2, 2, 64), 2.9e38)
+    x[1] = -1.0e38
+    zero = torch.zeros(2, 2, 64)
+    cache = ress_gpu.make_cache(1, 2, 64)
+    ress_gpu.ress_cache_append(zero.cuda(), x.cuda(), _i32([0, 1]), cache)
+    _ok(ress_gpu)
+    q = torch.ones(queries, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = ress_gpu.ress_cache_attn(q, cache, _i32([[0]]), _i32([2]), _i32([0, queries]))
+    _ok(ress_gpu)
+    held = (np64(cache.v) * np64(cache.v_scale)[:, :, None, None])[0, :, :2]
+    assert np.isfinite(held).all()
+    want = held.mean(axis=1)[None]
+    assert np.isfinite(np64(out)).all()
+    assert (np.abs(np64(out) - want) <= 2.0 ** -8 * np.abs(want)).all()
+    assert np.abs(np64(lse) - math.log(2)).max() <= 1e-5
