@@ -185,6 +185,7 @@ ress_status ress_cache_plan(const ress_cache_shape* shape, const int32_t* added,
   if (ress_status s = check_pool(shape, false)) return s;
   if (ress_status s = check_table(shape)) return s;
   if (n_free < 0 || tokens < 0) return RESS_ERR_INVALID_ARG;
+  if ((int64_t)tokens > kMaxTokens) return RESS_ERR_UNSUPPORTED;   // as attention over them
   if (!added || !lengths || !table || (n_free > 0 && !free_pages) || !cursor || !offsets ||
       (tokens > 0 && !slots) || !new_lengths || !new_cursor)
     return RESS_ERR_INVALID_ARG;

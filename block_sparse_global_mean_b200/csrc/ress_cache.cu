@@ -120,11 +120,12 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
     }
     return lo;
   };
-  const int stride = gridDim.x * kPlanThreads;
+  // (64 bits: a position within a stride of 2^31 would wrap past the end.)
+  const long long stride = gridDim.x * kPlanThreads;
   const int at = blockIdx.x * kPlanThreads + threadIdx.x;
   const int mask = p.page - 1;
 
-  for (int r = at; r <= p.requests; r += stride) {
+  for (long long r = at; r <= p.requests; r += stride) {
     p.offsets[r] = s_off[r];
     if (r < p.requests) {
       const int len = p.lengths[r];
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
   // New table entries.  Positions run over the pages asked for; those of a
   // request that failed are passed over.
   const int new_pages = min(s_first[p.requests], p.n_free);
-  for (int i = at; i < new_pages; i += stride) {
-    const int r = owner(s_first, i);
+  for (long long next = at; next < new_pages; next += stride) {
+    const int i = (int)next, r = owner(s_first, i);
     if (s_state[r] < 0) continue;
     const int old_pages = (s_state[r] + mask) >> p.page_log2;
     const int32_t id = p.free_pages[cursor + i];
@@ -147,7 +148,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
 
   // Slots.  The page of a token is an old table entry or the free-list entry
   // that the table gets, so nothing written above is read here.
-  for (int t = at; t < p.tokens; t += stride) {
+  for (long long next = at; next < p.tokens; next += stride) {
+    const int t = (int)next;
     int slot = -1;
     if (t < s_off[p.requests]) {
       const int r = owner(s_off, t);

@@ -577,7 +577,8 @@ typedef struct {
  *   added, lengths  [requests] int32;  table in/out;  free_pages [n_free] int32.
  *   cursor          [1] int32: first entry of free_pages not yet taken.
  *   offsets         out, [requests + 1] int32.
- *   slots           out, [tokens] int32; entries behind the added tokens get -1.
+ *   slots           out, [tokens] int32, tokens up to 2^30; entries behind the added
+ *                   tokens get -1.
  *   new_lengths     out, [requests] int32;  new_cursor  out, [1] int32.
  *   The outputs other than table must not overlap the inputs (every CTA reads
  *   the inputs while others write), which the call checks for equal pointers.

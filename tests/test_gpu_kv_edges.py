@@ -68,3 +68,15 @@ def test_attention_over_the_largest_numbers(queries, ress_gpu):
     assert np.isfinite(np64(out)).all()
     assert (np.abs(np64(out) - want) <= 2.0 ** -8 * np.abs(want)).all()
     assert np.abs(np64(lse) - math.log(2)).max() <= 1e-5
+
+
+def test_plan_with_the_longest_slot_map(ress_gpu):
+    """2^30 slots, all but the first few of no token."""
+    tokens = 1 << 30
+    off, slots, lengths, cursor = ress_gpu.ress_cache_plan(
+        _i32([5]), _i32([3]), _i32([[7, -1]]), _i32([1]), _i32([0]), 64, tokens)
+    _ok(ress_gpu)
+    assert slots.shape == (tokens,) and off.tolist() == [0, 5]
+    assert slots[:5].tolist() == list(range(7 * 64 + 3, 7 * 64 + 8))
+    assert int(slots[5:].max()) == -1 and int(slots[5:].min()) == -1
+    assert lengths.tolist() == [8] and int(cursor) == 0
