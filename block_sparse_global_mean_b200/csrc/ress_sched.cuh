@@ -97,14 +97,19 @@ struct SeqCost {
   __device__ __forceinline__ long long most() const { return base + slope * (tiles - 1); }
   __device__ __forceinline__ int pieces(long long share) const { return ceil_small(most(), share); }
 };
+// Chunks of `cols` columns.  (Unsigned: a cache row may hold up to 2^31 - 64 tokens,
+// and rounding that up to a chunk passes 2^31.)
+__device__ __forceinline__ int sched_round_up(const SchedParams& p, int cols) {
+  return (int)(((unsigned)cols + (1u << p.chunk_log2) - 1u) >> p.chunk_log2);
+}
 __device__ __forceinline__ long long sched_chunks_of(const SchedParams& p, int cols) {
-  return (long long)((cols + (1 << p.chunk_log2) - 1) >> p.chunk_log2) * p.mult;
+  return (long long)sched_round_up(p, cols) * p.mult;
 }
 __device__ __forceinline__ SeqCost sched_cost(const SchedParams& p, const SeqRange& r,
                                               const SeqRange& c) {
   SeqCost s{ceil_small((long long)r.rows * p.row_mult, p.tile_rows), 0, 0};
   if (p.step > 0 && p.step < r.rows) {
-    s.base = p.item_cost + max(c.valid - r.rows, 0) + p.tile_rows;
+    s.base = (long long)p.item_cost + max(c.valid - r.rows, 0) + p.tile_rows;
     s.slope = p.tile_rows;
   } else {
     s.base = p.item_cost + (sched_chunks_of(p, c.valid) << p.chunk_log2);
@@ -320,7 +325,7 @@ __device__ __forceinline__ long long sched_chunks(const SchedParams& p, const Se
                                                   const SeqRange& c, int tile) {
   if (p.step == 0) return sched_chunks_of(p, c.valid);
   const int last = min((tile + 1) * p.tile_rows, r.rows) - 1;
-  return (step_end(c.valid, r.rows, last, p.step) + (1 << p.chunk_log2) - 1) >> p.chunk_log2;
+  return sched_round_up(p, step_end(c.valid, r.rows, last, p.step));
 }
 
 // Piece `piece` of `ns` of an item's chunks.

@@ -80,3 +80,34 @@ def test_plan_with_the_longest_slot_map(ress_gpu):
     assert slots[:5].tolist() == list(range(7 * 64 + 3, 7 * 64 + 8))
     assert int(slots[5:].max()) == -1 and int(slots[5:].min()) == -1
     assert lengths.tolist() == [8] and int(cursor) == 0
+
+
+@pytest.mark.parametrize("step", [0, 1])
+@pytest.mark.parametrize("queries", [1, 128])
+def test_the_longest_request(queries, step, ress_gpu):
+    """2^31 - 64 cached tokens, which end inside a 128-key chunk: a table that names
+    two pages over and over, and another page at its end.  The keys of the two are
+    zero and those of the last one make logits of 32, so a row that sees none of it
+    gives the mean of the values 1 and 3 (sums of whole numbers, exact in float32 for
+    each CTA's share) and lse = ln of its keys, and a row that does gives the last
+    page's value 7 (the others weigh 2^31 e^-32 < 3e-5 of it) and 32 + ln of the
+    last page's keys it sees, both to the 3e-5 and bf16's rounding."""
+    page, n = 64, 2 ** 31 - 64
+    pages = n // page
+    cache = ress_gpu.make_cache(3, 1, page)
+    for c in (cache.k_scale, cache.v_scale):
+        c.fill_(1.0)
+    for i, (key, value) in enumerate(((0.0, 1.0), (0.0, 3.0), (4.0, 7.0))):
+        cache.k[i], cache.v[i] = torch.tensor(key).to(FP8), torch.tensor(value).to(FP8)
+    table = (torch.arange(pages, dtype=torch.int32, device="cuda") & 1)[None].contiguous()
+    table[0, -1] = 2
+    q = torch.ones(queries, 1, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = ress_gpu.ress_cache_attn(q, cache, table, _i32([n]), _i32([0, queries]), step=step)
+    _ok(ress_gpu)
+    at = np.arange(queries) - queries      # positions from the end
+    seen = np.full(queries, 64) if step == 0 else np.maximum(at + 65, 0)
+    for i in range(queries):
+        want = 7.0 if seen[i] else 2.0
+        wlse = 32 + math.log(seen[i]) if seen[i] else math.log(n + int(at[i]) + 1)
+        assert (np.abs(np64(out)[i] - want) <= want * (2.0 ** -8 + 3e-5)).all(), i
+        assert abs(float(lse[0, i]) - wlse) <= 3e-5 + 1e-5 * wlse, i
