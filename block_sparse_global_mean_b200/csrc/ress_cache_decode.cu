@@ -110,7 +110,9 @@ __device__ __forceinline__ float query_f16(uint4 a, uint4 b, uint32_t (&w)[8]) {
   for (int i = 0; i < 8; ++i) top = max(top, max((u[i] << 16) & 0x7f800000u, u[i] & 0x7f800000u));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  const int e = min(max((int)(top >> 23) - 127, -100), 100);
+  // Any bf16 number: both powers of two below are normal ones from 2^-112 on, and rows
+  // of smaller values only lose depth below their largest.
+  const int e = min(max((int)(top >> 23) - 127, -112), 127);
   const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i)

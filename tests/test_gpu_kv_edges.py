@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from tests.kv_reference import cache_attention, check_cache_attention
 from tests.parity import np64
 
 pytestmark = pytest.mark.gpu
@@ -111,3 +112,24 @@ def test_the_longest_request(queries, step, ress_gpu):
         wlse = 32 + math.log(seen[i]) if seen[i] else math.log(n + int(at[i]) + 1)
         assert (np.abs(np64(out)[i] - want) <= want * (2.0 ** -8 + 3e-5)).all(), i
         assert abs(float(lse[0, i]) - wlse) <= 3e-5 + 1e-5 * wlse, i
+
+
+@pytest.mark.parametrize("queries", [1, 70])
+@pytest.mark.parametrize("up", [102, 106, -100, -113])
+def test_queries_of_any_magnitude(up, queries, ress_gpu):
+    """Queries of magnitudes around 2^up and keys around 2^-up, so that the logits are
+    of order one, with one query row of ones beside the large ones (logits of zero)."""
+    g = torch.Generator().manual_seed(up + queries)
+    n, heads = 150, 2
+    x = torch.randn(n, 1, 64, generator=g) * 2.0 ** -up
+    v = torch.randn(n, 1, 64, generator=g)
+    cache = ress_gpu.make_cache(3, 1, 64)
+    ress_gpu.ress_cache_append(x.cuda(), v.cuda(),
+                               torch.arange(n, dtype=torch.int32, device="cuda"), cache)
+    q = (torch.randn(queries, heads, 64, generator=g) * 2.0 ** up).to(torch.bfloat16)
+    if up > 0:
+        q[0, 1] = 1.0
+    out, lse = ress_gpu.ress_cache_attn(q.cuda(), cache, _i32([[0, 1, 2]]), _i32([n]),
+                                        _i32([0, queries]))
+    _ok(ress_gpu)
+    check_cache_attention(out, lse, cache_attention(q, cache, [[0, 1, 2]], [n], [0, queries]))
