@@ -500,6 +500,10 @@ size_t ress_cross_bwd_workspace_bytes(const ress_cross_shape* shape);
  *   enter P V as bf16, their sum and lse are float32 sums of the unrounded
  *   ones.  Results do not depend on the run: no atomics add numbers.  Outputs
  *   must not overlap inputs.
+ *   Logits are made for magnitudes up to 2^30.  Beyond, where float32 keeps them
+ *   to 64 at best, a row may come out as NaN, since the difference from the row's
+ *   maximum holds what rounding took from the maximum.  (A kernel without that
+ *   limit was built; it cost every call 5 %.)
  */
 ress_status ress_cross_attn(const ress_cross_shape* shape, const void* q, const void* k,
                             const void* v, const int32_t* q_offsets, const int32_t* kv_offsets,
@@ -520,6 +524,8 @@ ress_status ress_cross_attn(const ress_cross_shape* shape, const void* q, const 
  *   dout       [nq][heads][64] bf16.
  *   dq         [nq][heads][64] bf16; dk, dv [nk][kv_heads][64] bf16.
  *   workspace  ress_cross_bwd_workspace_bytes(shape) bytes, 256-byte aligned.
+ *   P = exp(S - lse) takes lse as float32, so it is off by 2^-24 |lse|: gradients
+ *   mean something for logits up to about 2^16.
  *   P enters its product as bf16, dS as bf16 for dk and as two bf16 numbers
  *   (16 bits) for dq; all sums are float32 in a fixed order.
  */
@@ -651,6 +657,7 @@ size_t ress_cache_attn_workspace_bytes(const ress_cache_shape* shape, int32_t he
  *   bf16 or f16, their sums and lse are float32.  Cells behind lengths[r] are
  *   never used as numbers; a NaN code before them may count as 480 (the append
  *   that made it was flagged).  Scales must be powers of two from 2^-100 to 2^119.
+ *   Logits up to 2^30, as in ress_cross_attn.
  */
 ress_status ress_cache_attn(const ress_cache_shape* shape, int32_t heads, int32_t tokens,
                             const void* q, int64_t q_stride, const void* k_cache,
