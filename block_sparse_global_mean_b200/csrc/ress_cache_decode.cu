@@ -96,6 +96,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Nonzero if one of four codes is NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -260,6 +265,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           }
         }
         const int lim0 = end0 - pos, lim1 = end1 - pos;
+        const int left = seg.cols_valid - pos;
         if (__any_sync(0xffffffffu, lim0 < kKeys || lim1 < kKeys)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -267,6 +273,36 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             if (8 * j + v_row1 >= lim0) x[j][1] = -INFINITY;
             if (8 * j + v_row0 >= lim1) x[j][2] = -INFINITY;
             if (8 * j + v_row1 >= lim1) x[j][3] = -INFINITY;
+          }
+          // Where one row sees keys that another does not, a NaN value would reach both
+          // (0 * NaN): it leaves the value and goes into the logits of the rows that see
+          // its token.
+          const int most = min(left, kKeys);
+          if (__any_sync(0xffffffffu, lim0 < most || lim1 < most)) {
+            uint4* row = reinterpret_cast<uint4*>(ring + s * 2 * kHalf + kHalf + lane * 64);
+            uint32_t nan = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 w = row[u];
+              nan |= nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
+            }
+            const unsigned bad = __ballot_sync(0xffffffffu, nan != 0);
+            if (bad != 0) {
+              if (nan != 0) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) row[u] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();   // the next copy into this place comes after it
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int k0 = 8 * j + v_row0, k1 = 8 * j + v_row1;
+                if ((bad >> k0 & 1u) && k0 < lim0) x[j][0] = __int_as_float(0x7fffffff);
+                if ((bad >> k1 & 1u) && k1 < lim0) x[j][1] = __int_as_float(0x7fffffff);
+                if ((bad >> k0 & 1u) && k0 < lim1) x[j][2] = __int_as_float(0x7fffffff);
+                if ((bad >> k1 & 1u) && k1 < lim1) x[j][3] = __int_as_float(0x7fffffff);
+              }
+            }
           }
         }
         // Chunk maximum, probabilities, sums.
@@ -317,7 +353,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           l1 = fmaf(b1, s1, a1 * l1);
         }
         // O = a O + b scale (P V).
-        const int left = seg.cols_valid - pos;
         const bool tail = left < kKeys;
         float y[8][4];
 #pragma unroll
@@ -370,6 +405,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // A NaN value has reached its own dimension: it goes to the row's sum, and so to
+    // all of the row, as a NaN key does.
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      bool nan = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        nan |= isnan(o[j][2 * half]) || isnan(o[j][2 * half + 1]);
+      const unsigned who = __ballot_sync(0xffffffffu, nan);
+      if (who >> (lane & 28) & 15u) (half ? l1 : l0) = __int_as_float(0x7fffffff);
+    }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const bool live = half ? live1 : live0;

@@ -655,8 +655,9 @@ size_t ress_cache_attn_workspace_bytes(const ress_cache_shape* shape, int32_t he
  *   workspace ress_cache_attn_workspace_bytes() bytes, 256-byte aligned.
  *   Codes and queries are multiplied exactly; probabilities enter P V as
  *   bf16 or f16, their sums and lse are float32.  Cells behind lengths[r] are
- *   never used as numbers; a NaN code before them may count as 480 (the append
- *   that made it was flagged).  Scales must be powers of two from 2^-100 to 2^119.
+ *   never used as numbers.  A token before them whose key or value holds a NaN
+ *   code (the append that made it was flagged) makes NaN every row that sees it,
+ *   all 64 values and lse, and changes no other row.  Scales must be powers of two from 2^-100 to 2^119.
  *   Logits up to 2^30, as in ress_cross_attn.
  */
 ress_status ress_cache_attn(const ress_cache_shape* shape, int32_t heads, int32_t tokens,
