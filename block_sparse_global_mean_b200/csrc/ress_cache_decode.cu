@@ -234,6 +234,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         qs0 = query_f16(a0, b0, q0);
         qs1 = query_f16(a1, b1, q1);
       }
+      // Pages of a wrong scale are masked: their copies are on the way (the scales
+      // looked at before them cost 1 us of every call).
+      if (!scale_ok(ks) || !scale_ok(vs)) {
+        raise_device_error(p.err, RESS_ERR_INVALID_ARG, 96);
+        ks = -1.f;
+        vs = 0.f;
+      }
       while (to_use != 0) {
         const int c = __ffs((int)to_use) - 1;
         to_use &= to_use - 1u;
@@ -264,9 +271,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
             mma_f16(x[j], a, b0, b1);
           }
         }
-        const int lim0 = end0 - pos, lim1 = end1 - pos;
+        int lim0 = end0 - pos, lim1 = end1 - pos;
         const int left = seg.cols_valid - pos;
-        if (__any_sync(0xffffffffu, lim0 < kKeys || lim1 < kKeys)) {
+        if (__any_sync(0xffffffffu, lim0 < kKeys || lim1 < kKeys || kscale < 0.f)) {
+          if (kscale < 0.f) lim0 = lim1 = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (8 * j + v_row0 >= lim0) x[j][0] = -INFINITY;

@@ -46,6 +46,13 @@ __device__ __forceinline__ int step_end(int len, int n, int i, int step) {
   return end < len ? (int)end : len;
 }
 
+// Scales of cache pages: powers of two from 2^-100 to 2^119, so that both ways to take
+// a code to code * scale are exact, or zero (a page that was never written).
+__device__ __forceinline__ bool scale_ok(float scale) {
+  const uint32_t b = __float_as_uint(scale);
+  return b == 0u || ((b & 0x7fffffu) == 0u && b - (27u << 23) <= (219u << 23));
+}
+
 // Programmatic dependent launch: a kernel is launched while the one before it on
 // the stream still runs, sets itself up, and waits here for its results.  What it
 // reads may be written while it lives, so it reads global memory with plain loads,

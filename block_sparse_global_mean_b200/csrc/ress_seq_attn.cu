@@ -97,7 +97,7 @@ struct __align__(8) Ctl {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  int page_ok[kMaxStages][2];   // cache: the 64-key halves of a stage come from a page of the pool
+  int page_ok[kMaxStages][2];   // cache: a 64-key half of a stage comes from a page that counts
   Segment seg[2];
   float odd_m[128];
   float odd_l[128];
@@ -652,8 +652,13 @@ __global__ void __launch_bounds__((Cfg<kPair, kCache>::threads), 1)
         uint4 kcur[4], vcur[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) kcur[u] = kw[u], vcur[u] = vw[u];
-        const float kscale = ks, vscale = vs;
-        const bool hole_now = hole;
+        float kscale = ks, vscale = vs;
+        bool hole_now = hole;
+        if (!scale_ok(kscale) || !scale_ok(vscale)) {   // left out, like a page of no pool
+          raise_device_error(p.err, RESS_ERR_INVALID_ARG, 96);
+          kscale = vscale = 0.f;
+          hole_now = true;
+        }
         // The next chunk's codes, and the page of the one behind it, are on
         // their way while this one is converted.
         if (c + 1 < n) fetch(id_next, pos + kChunk);

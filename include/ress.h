@@ -650,15 +650,16 @@ size_t ress_cache_attn_workspace_bytes(const ress_cache_shape* shape, int32_t he
  *             [requests + 1] int32.  Flagged as RESS_ERR_BAD_INDEX: offsets
  *             out of range or descending (detail 90; the request is taken as
  *             empty), a length outside 0 .. max_pages * page (94; clamped), a
- *             page outside the pool (95; its keys are left out).
+ *             page outside the pool (95; its keys are left out).  Scales must be
+ *             powers of two from 2^-100 to 2^119, or zero; a page with another one
+ *             is flagged (RESS_ERR_INVALID_ARG, detail 96) and its keys are left out.
  *   out       [tokens][heads][64] bf16;  lse [heads][tokens] float32 or NULL.
  *   workspace ress_cache_attn_workspace_bytes() bytes, 256-byte aligned.
  *   Codes and queries are multiplied exactly; probabilities enter P V as
  *   bf16 or f16, their sums and lse are float32.  Cells behind lengths[r] are
  *   never used as numbers.  A token before them whose key or value holds a NaN
  *   code (the append that made it was flagged) makes NaN every row that sees it,
- *   all 64 values and lse, and changes no other row.  Scales must be powers of two from 2^-100 to 2^119.
- *   Logits up to 2^30, as in ress_cross_attn.
+ *   all 64 values and lse, and changes no other row.  Logits up to 2^30, as in ress_cross_attn.
  */
 ress_status ress_cache_attn(const ress_cache_shape* shape, int32_t heads, int32_t tokens,
                             const void* q, int64_t q_stride, const void* k_cache,

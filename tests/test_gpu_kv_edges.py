@@ -9,6 +9,7 @@ import torch
 
 from tests.kv_reference import cache_attention, check_cache_attention
 from tests.parity import np64
+from tests.test_gpu_cache import make_requests
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +134,41 @@ def test_queries_of_any_magnitude(up, queries, ress_gpu):
                                         _i32([0, queries]))
     _ok(ress_gpu)
     check_cache_attention(out, lse, cache_attention(q, cache, [[0, 1, 2]], [n], [0, queries]))
+
+
+@pytest.mark.parametrize("queries", [1, 150])
+@pytest.mark.parametrize("part", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("scale", [3.0, 2.0 ** -101, 2.0 ** 120, -1.0, math.inf, math.nan, 1e-40])
+def test_pages_of_a_wrong_scale_are_flagged_and_left_out(scale, part, queries, ress_gpu):
+    lengths = [300, 200]
+    q, cache, table, off = make_requests(ress_gpu, lengths, [queries] * 2, 64, 4, 2, seed=23)
+    args = _i32(table), _i32(lengths), _i32(off)
+    for page in (table[0][2], table[1][3]):          # inside a request, and its last one
+        getattr(cache, part)[page, 1] = scale
+    out, lse = ress_gpu.ress_cache_attn(q.cuda(), cache, *args)
+    assert ress_gpu.ress_check_device_errors() == (ress_gpu.RESS_ERR_INVALID_ARG, 96)
+    for head in range(2):                            # the other key head keeps its pages
+        t = [list(row) for row in table]
+        if head == 1:
+            t[0][2], t[1][3] = -1, -1
+        one = type(cache)(*(x[:, head:head + 1].contiguous() for x in cache))
+        h = slice(2 * head, 2 * head + 2)
+        one.k_scale[~torch.isfinite(one.k_scale)], one.v_scale[~torch.isfinite(one.v_scale)] = 1., 1.
+        ref = cache_attention(q[:, h], one, t, lengths, off)
+        check_cache_attention(out[:, h], lse[h], ref)
+
+
+@pytest.mark.parametrize("queries", [1, 150])
+def test_scales_of_zero_and_at_the_ends_are_taken(queries, ress_gpu):
+    """A page that was never written stands for zeros; 2^-100 and 2^119 are scales."""
+    q, cache, table, off = make_requests(ress_gpu, [200], [queries], 64, 2, 1, seed=29)
+    cache.k_scale[table[0][0]], cache.v_scale[table[0][0]] = 0.0, 0.0
+    cache.k_scale[table[0][1]], cache.v_scale[table[0][1]] = 2.0 ** -100, 2.0 ** -100
+    out, lse = ress_gpu.ress_cache_attn(q.cuda(), cache, _i32(table), _i32([200]), _i32(off))
+    _ok(ress_gpu)
+    check_cache_attention(out, lse, cache_attention(q, cache, table, [200], off))
+    cache.v_scale[table[0][2]] = 2.0 ** 119
+    cache.v.view(torch.uint8)[table[0][2]] &= 0x8F      # codes below 2^-5: sums stay in float32
+    out, lse = ress_gpu.ress_cache_attn(q.cuda(), cache, _i32(table), _i32([200]), _i32(off))
+    _ok(ress_gpu)
+    check_cache_attention(out, lse, cache_attention(q, cache, table, [200], off))
