@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -612,9 +613,17 @@ except ImportError:
     _call = None
 
 
+def _int32(**numbers) -> None:
+    """ctypes cuts integers to their low 32 bits without a word."""
+    for name, x in numbers.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must fit in 32 bits, got {x}")
+
+
 @functools.lru_cache(maxsize=1024)
 def _cross_shape(nq: int, nk: int, seqs: int, heads: int, kv_heads: int, head_dim: int,
                  q_stride: int, k_stride: int, v_stride: int):
+    _int32(sequences=seqs, heads=heads, kv_heads=kv_heads, head_dim=head_dim)
     sh = ctypes.byref(ress_cross_shape(nq, nk, seqs, heads, kv_heads, head_dim, RESS_BF16,
                                        q_stride, k_stride, v_stride))
     return (sh, int(lib.ress_cross_workspace_bytes(sh)),
@@ -624,12 +633,15 @@ def _cross_shape(nq: int, nk: int, seqs: int, heads: int, kv_heads: int, head_di
 @functools.lru_cache(maxsize=1024)
 def _cache_shape(pages: int, page: int, kv_heads: int, head_dim: int, requests: int,
                  max_pages: int):
+    _int32(pages=pages, page=page, kv_heads=kv_heads, head_dim=head_dim, requests=requests,
+           max_pages=max_pages)
     return ctypes.byref(ress_cache_shape(pages, page, kv_heads, head_dim, requests, max_pages))
 
 
 @functools.lru_cache(maxsize=1024)
 def _cache_attn_bytes(pages: int, page: int, kv_heads: int, head_dim: int, requests: int,
                       max_pages: int, heads: int, tokens: int) -> int:
+    _int32(heads=heads, tokens=tokens)
     sh = _cache_shape(pages, page, kv_heads, head_dim, requests, max_pages)
     return int(lib.ress_cache_attn_workspace_bytes(sh, heads, tokens))
 
@@ -877,7 +889,9 @@ def ress_cache_plan(added: torch.Tensor, lengths: torch.Tensor, table: torch.Ten
     device, i32 = added.device, torch.int32
     if added.dim() != 1 or table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("added must be [R], table [R, max_pages], free_pages [n]")
-    (r, width), tokens = table.shape, int(tokens)
+    (r, width), page, tokens = table.shape, operator.index(page), operator.index(tokens)
+    limit = (2 ** 31 - 1) // max(page, 1) if pages is None else operator.index(pages)
+    _int32(page=page, pages=limit, tokens=tokens, free_pages=free_pages.shape[0])
     ins = (_expect(added, (r,), i32, device, "added"),
            _expect(lengths, (r,), i32, device, "lengths"),
            _expect(table, (r, width), i32, device, "table"),
@@ -893,9 +907,8 @@ def ress_cache_plan(added: torch.Tensor, lengths: torch.Tensor, table: torch.Ten
                               (offsets, slots, new_lengths, new_cursor), sizes):
             made.append(_new((n,), i32, added, stream) if t is None else t)
             ptrs.append(_expect(made[-1], (n,), i32, device, name))
-    limit = (2 ** 31 - 1) // max(int(page), 1) if pages is None else pages
     _check(_run_on(device, stream, lib.ress_cache_plan,
-                   _cache_shape(limit, int(page), 1, 64, r, width), *ins, tokens, *ptrs),
+                   _cache_shape(limit, page, 1, 64, r, width), *ins, tokens, *ptrs),
            "ress_cache_plan")
     return made[0], made[1], made[2], made[3]
 
@@ -915,6 +928,7 @@ def ress_cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cac
                          f"{tuple(v.shape)}")
     _check_rows(v, "v", device, heads, (k.dtype,))
     n = k.shape[0]
+    _int32(tokens=n)
     _check(_run_on(device, stream, lib.ress_cache_append,
                    _cache_shape(pages, page, heads, d, 1, 1), k.data_ptr(), v.data_ptr(),
                    RESS_F32 if k.dtype is torch.float32 else RESS_BF16, _token_rows(k, "k"),
@@ -948,7 +962,8 @@ def ress_cache_attn(q: torch.Tensor, cache: ress_cache, table: torch.Tensor,
         raise ValueError(f"q has head dim {dq}, the cache {d}")
     if table.dim() != 2:
         raise ValueError("table must be [requests, max_pages]")
-    r, width = table.shape
+    (r, width), step = table.shape, operator.index(step)
+    _int32(step=step)
     arrays = (_expect(table, (r, width), i32, device, "table"),
               _expect(lengths, (r,), i32, device, "lengths"),
               _expect(offsets, (r + 1,), i32, device, "offsets"))
@@ -957,7 +972,7 @@ def ress_cache_attn(q: torch.Tensor, cache: ress_cache, table: torch.Tensor,
                                q, stream)
     _check(_run_on(device, stream, lib.ress_cache_attn,
                    _cache_shape(pages, page, heads, d, r, width), h, n, q.data_ptr(),
-                   _token_rows(q, "q"), *parts, *arrays, int(step), out_ptr, lse_ptr, ws, size),
+                   _token_rows(q, "q"), *parts, *arrays, step, out_ptr, lse_ptr, ws, size),
            "ress_cache_attn")
     return out, lse
 
