@@ -11,7 +11,6 @@ bool aligned(const void* p, uintptr_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
-constexpr int kMaxSeqs = 8192;
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;
 
 // Row stride in elements (0: dense rows of `width`); 0 back when it is invalid.

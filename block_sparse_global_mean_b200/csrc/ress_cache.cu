@@ -2,6 +2,7 @@
 // writer (append).
 #include "ress_common.cuh"
 #include "ress_internal.h"
+#include "ress_kv.h"
 #include "ress_seq.cuh"
 
 namespace ress {
@@ -422,10 +423,14 @@ ress_status launch_cache_plan(const ress_cache_shape& s, const int32_t* added,
   p.pages = s.pages;
   p.n_free = n_free;
   p.tokens = tokens;
-  const size_t smem = sizeof(int32_t) * (3 * (size_t)s.requests + 2);
+  auto smem_of = [](int requests) { return sizeof(int32_t) * (3 * (size_t)requests + 2); };
+  const size_t smem = smem_of(s.requests);
+  // Once and for the most requests that a call may have: set to each call's own size,
+  // another thread's call could lower it before this one's launch.
+  static std::atomic<uint64_t> allowed{0};
   if (smem > 48 * 1024)
-    if (ress_status e = record_cuda(cudaFuncSetAttribute(
-            cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
+    if (ress_status e = allow_smem(reinterpret_cast<const void*>(cache_plan_kernel),
+                                   smem_of(kMaxSeqs), &allowed))
       return e;
   const long long items = (long long)tokens + s.requests;
   const long long blocks = (items + 4 * kPlanThreads - 1) / (4 * kPlanThreads);

@@ -5,6 +5,8 @@
 
 namespace ress {
 
+constexpr int kMaxSeqs = 8192;   // sequences, requests
+
 // Validated shape of ress_cross_attn and ress_cross_attn_bwd.
 struct CrossGeometry {
   int nq, nk, seqs, heads, kv_heads, group;

@@ -172,3 +172,32 @@ def test_scales_of_zero_and_at_the_ends_are_taken(queries, ress_gpu):
     out, lse = ress_gpu.ress_cache_attn(q.cuda(), cache, _i32(table), _i32([200]), _i32(off))
     _ok(ress_gpu)
     check_cache_attention(out, lse, cache_attention(q, cache, table, [200], off))
+
+
+def test_plans_of_many_requests_from_two_threads(ress_gpu):
+    """Plans that need more shared memory than a kernel has by default, of different
+    sizes, from two threads at once."""
+    import threading
+    sizes, failed = (8192, 4200), []
+    ins = [(_i32([1] * r), _i32([0] * r), torch.full((r, 1), -1, dtype=torch.int32, device="cuda"),
+            torch.arange(r, dtype=torch.int32, device="cuda"), _i32([0])) for r in sizes]
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            for _ in range(400):
+                off, slots, lengths, cursor = ress_gpu.ress_cache_plan(
+                    *ins[i], 64, sizes[i], stream=streams[i])
+            streams[i].synchronize()
+            assert torch.equal(slots, torch.arange(sizes[i], dtype=torch.int32, device="cuda") * 64)
+        except Exception as e:   # (a thread's exception would pass unseen)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _ok(ress_gpu)
+    assert not failed, failed
