@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
+#include <string.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/ress.h"
@@ -32,10 +33,15 @@ bool find(void* lib, const char* name, F* f) {
   return *f != nullptr;
 }
 
-// init(path of the library, which is loaded already)
-PyObject* init(PyObject*, PyObject* path) {
-  const char* p = PyUnicode_AsUTF8(path);
-  if (p == nullptr) return nullptr;
+// init(path of the library, which is loaded already, and the tag of this torch and
+// Python: another one's objects would be read by the layouts compiled in here)
+PyObject* init(PyObject*, PyObject* args) {
+  const char *p, *tag;
+  if (!PyArg_ParseTuple(args, "ss", &p, &tag)) return nullptr;
+  if (strcmp(tag, RESS_CALL_TAG) != 0) {
+    PyErr_Format(PyExc_ImportError, "built for %s, not for %s", RESS_CALL_TAG, tag);
+    return nullptr;
+  }
   void* lib = dlopen(p, RTLD_NOW);
   if (lib == nullptr || !find(lib, "ress_cross_workspace_bytes", &cross_bytes) ||
       !find(lib, "ress_cross_bwd_workspace_bytes", &cross_bwd_bytes) ||
@@ -364,7 +370,7 @@ constexpr PyCFunction as_c(F f) {
 }
 
 PyMethodDef methods[] = {
-    {"init", init, METH_O, nullptr},
+    {"init", init, METH_VARARGS, nullptr},
     {"cross_attn", as_c(py_cross_attn), METH_FASTCALL, nullptr},
     {"cross_attn_bwd", as_c(py_cross_attn_bwd), METH_FASTCALL, nullptr},
     {"cache_plan", as_c(py_cache_plan), METH_FASTCALL, nullptr},

@@ -608,7 +608,8 @@ def ress_validate_idx(idx: torch.Tensor, n: int, block: int,
 # --------------------------------------------------------------------------------------------
 try:   # the common calls in C++ (csrc/ress_call.cpp); without it all of them are made below
     from . import _ress_call as _call
-    _call.init(LIB_PATH)
+    from .build import call_tag
+    _call.init(LIB_PATH, call_tag())
 except ImportError:
     _call = None
 
