@@ -24,7 +24,13 @@
 // zero: with keys whose mean is twice their spread a single bf16 dS left 0.41 %
 // in dQ against 0.17 % of the output's own rounding.  The query walk therefore
 // multiplies dS as two bf16 numbers, its rounding and the rest (16 bits of it).
-// dK and dV have no such sum; they are off by 0.23 %.
+// dK and dV have no such sum; over many keys they are off by 0.24 %, by the output's
+// rounding and that of P or dS.  Over few keys a key's probabilities may all stand
+// where bf16's steps are widest, and 0.35 % was met (one head, 100 queries, 33 keys).
+// So over up to a tile of keys the key walk makes every chunk twice, with the
+// roundings and with the rests: 0.17 %, as much as the output's own rounding.  It
+// costs 1,374 queries against 128 keys 48 us for 39, 140,800 against 5 keys 1.51 ms
+// for 1.08 (16 heads).
 //
 // TMEM (512 columns): X of the two softmax groups (2 x 128; P, or the rest of dS,
 // and dS as bf16 over it once it is in registers), one Y (128, free again when it
@@ -46,6 +52,8 @@
 #include "ress_kv.h"
 #include "ress_sched.cuh"
 
+#include <type_traits>
+
 namespace ress {
 
 namespace {
@@ -58,6 +66,7 @@ constexpr uint32_t kStageBytes = 2 * kTileBytes;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColY = 256, kColA1 = 384, kColA2 = 448;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTwiceKeys = 129;   // fewer keys than this: every chunk twice
 
 struct BwdParams {
   SchedParams sched[2];      // key walk, query walk
@@ -201,6 +210,9 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
     tc_fence_after();
     return *abortf == 0;
   };
+  // Few keys: every chunk twice, first with P and dS rounded to bf16, then with what
+  // that left (1: shift of the item's chunks).
+  auto twice = [&](const Segment& g) { return !kDQ && g.rows_valid < kTwiceKeys ? 1 : 0; };
   // Chunk c of an item: its column rows (and, in the key walk, its query head).
   auto chunk_at = [&](const Segment& g, int c, int& col, int& head) {
     if (kDQ) {
@@ -208,6 +220,7 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
       head = g.head;
     } else {
       const int per = (g.cols_valid + kChunk - 1) / kChunk;
+      c >>= twice(g);
       const int h = c / per;
       col = (c - h * per) * kChunk;
       head = g.head * p.group + h;
@@ -418,7 +431,7 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
       const Segment& g = ctl->seg[s & 1];
       if (g.kind == 0) break;
       const int kind = g.kind, c0 = g.c0, n = g.c1 - g.c0, cols = g.cols_valid;
-      const int per = (cols + kChunk - 1) / kChunk;
+      const int per = (cols + kChunk - 1) / kChunk, tw = twice(g);
       const int tok = g.tile * sp.tile_rows + tok_in_tile;
       const bool live = in_tile && tok < g.rows;
       const bool real = in_tile && tok < g.rows_valid;
@@ -433,7 +446,7 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
       for (int i = par; i < n; i += 2, ++cnt) {
         const uint32_t ph = (uint32_t)cnt & 1u;
         const int kc = kc0 + i, st = kc % kStages;
-        const int left = cols - (kDQ ? c0 + i : (c0 + i) % per) * kChunk;
+        const int left = cols - (kDQ ? c0 + i : ((c0 + i) >> tw) % per) * kChunk;
         if (!warp_wait(bar_x + 8u * (uint32_t)par, ph, abortf, p.err, 170)) {
           ok = false;
           break;
@@ -493,53 +506,64 @@ __device__ __forceinline__ void bwd_walk(const CUtensorMap* tm_a1, const CUtenso
           }
           fence_proxy_async_smem();
         }
-        uint32_t y[2][16];
-        tmem_ld16(tY, y[0]);
+        auto operands = [&](auto rest_c) {
+          constexpr bool kRest = decltype(rest_c)::value;
+          uint32_t y[2][16];
+          tmem_ld16(tY, y[0]);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16], dk[16];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16], dk[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {   // 16 columns of Y
-            tmem_ld_wait_regs16(y[h]);
-            if (2 * q + h < 7) {
-              tmem_ld16(tY + 16 * (2 * q + h + 1), y[h ^ 1]);
-            } else {
-              tc_fence_before();
-              mbar_arrive(bar_yf + 8u * (uint32_t)par);
-            }
-            if (left < kChunk) {
-#pragma unroll
-              for (int u = 0; u < 16; ++u)
-                if (32 * q + 16 * h + u >= left) y[h][u] = 0u;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float4 nd4 = make_float4(nd_row, nd_row, nd_row, nd_row);
-              if (!kDQ) nd4 = reinterpret_cast<const float4*>(ctl->nd[st])[8 * q + 4 * h + e];
-              const uint32_t* pr = &r[q][16 * h + 4 * e];
-              const float2 p0 = make_float2(__uint_as_float(pr[0]), __uint_as_float(pr[1]));
-              const float2 p1 = make_float2(__uint_as_float(pr[2]), __uint_as_float(pr[3]));
-              const float2 d0 = fmul2(p0, fadd2(make_float2(__uint_as_float(y[h][4 * e]),
-                                                            __uint_as_float(y[h][4 * e + 1])),
-                                                make_float2(nd4.x, nd4.y)));
-              const float2 d1 = fmul2(p1, fadd2(make_float2(__uint_as_float(y[h][4 * e + 2]),
-                                                            __uint_as_float(y[h][4 * e + 3])),
-                                                make_float2(nd4.z, nd4.w)));
-              const int at = 8 * h + 2 * e;
-              dk[at] = pack_bf16x2(d0.x, d0.y);
-              dk[at + 1] = pack_bf16x2(d1.x, d1.y);
-              if (kDQ) {   // what the rounding leaves
-                pk[at] = rest_bf16x2(d0, dk[at]);
-                pk[at + 1] = rest_bf16x2(d1, dk[at + 1]);
+            for (int h = 0; h < 2; ++h) {   // 16 columns of Y
+              tmem_ld_wait_regs16(y[h]);
+              if (2 * q + h < 7) {
+                tmem_ld16(tY + 16 * (2 * q + h + 1), y[h ^ 1]);
               } else {
-                pk[at] = pack_bf16x2(p0.x, p0.y);
-                pk[at + 1] = pack_bf16x2(p1.x, p1.y);
+                tc_fence_before();
+                mbar_arrive(bar_yf + 8u * (uint32_t)par);
+              }
+              if (left < kChunk) {
+#pragma unroll
+                for (int u = 0; u < 16; ++u)
+                  if (32 * q + 16 * h + u >= left) y[h][u] = 0u;
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float4 nd4 = make_float4(nd_row, nd_row, nd_row, nd_row);
+                if (!kDQ) nd4 = reinterpret_cast<const float4*>(ctl->nd[st])[8 * q + 4 * h + e];
+                const uint32_t* pr = &r[q][16 * h + 4 * e];
+                const float2 p0 = make_float2(__uint_as_float(pr[0]), __uint_as_float(pr[1]));
+                const float2 p1 = make_float2(__uint_as_float(pr[2]), __uint_as_float(pr[3]));
+                const float2 d0 = fmul2(p0, fadd2(make_float2(__uint_as_float(y[h][4 * e]),
+                                                              __uint_as_float(y[h][4 * e + 1])),
+                                                  make_float2(nd4.x, nd4.y)));
+                const float2 d1 = fmul2(p1, fadd2(make_float2(__uint_as_float(y[h][4 * e + 2]),
+                                                              __uint_as_float(y[h][4 * e + 3])),
+                                                  make_float2(nd4.z, nd4.w)));
+                const int at = 8 * h + 2 * e;
+                dk[at] = pack_bf16x2(d0.x, d0.y);
+                dk[at + 1] = pack_bf16x2(d1.x, d1.y);
+                if (kDQ) {   // what the rounding leaves
+                  pk[at] = rest_bf16x2(d0, dk[at]);
+                  pk[at + 1] = rest_bf16x2(d1, dk[at + 1]);
+                } else {
+                  pk[at] = pack_bf16x2(p0.x, p0.y);
+                  pk[at + 1] = pack_bf16x2(p1.x, p1.y);
+                }
+                if (kRest) {
+                  dk[at] = rest_bf16x2(d0, dk[at]);
+                  dk[at + 1] = rest_bf16x2(d1, dk[at + 1]);
+                  pk[at] = rest_bf16x2(p0, pk[at]);
+                  pk[at + 1] = rest_bf16x2(p1, pk[at + 1]);
+                }
               }
             }
+            tmem_st16(tX + 16 * q, pk);
+            tmem_st16(tX + 64 + 16 * q, dk);
           }
-          tmem_st16(tX + 16 * q, pk);
-          tmem_st16(tX + 64 + 16 * q, dk);
-        }
+        };
+        if (!kDQ && (tw & (c0 + i)) != 0) operands(std::true_type{});
+        else operands(std::false_type{});
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar_p + 8u * (uint32_t)par);
@@ -709,6 +733,7 @@ ress_status launch_cross_bwd(const CrossGeometry& g, CrossBwdParams c, void* ws,
     s.heads = g.kv_heads;
     s.tile_rows = dq ? p.tps : 128;
     s.mult = dq ? 1 : g.group;
+    s.twice_rows = dq ? 0 : kTwiceKeys;
     s.row_mult = 1;
     s.chunk_log2 = kChunkLog2;
     s.item_cost = 5 * kChunk;   // a ragged batch: 165 us at 2 chunks, 151 us at 5

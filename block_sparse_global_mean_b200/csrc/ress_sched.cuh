@@ -49,6 +49,7 @@ struct SchedParams {
   int row_mult;               // item rows per sequence row
   int tile_rows;              // item rows of a tile
   int mult;                   // passes over the columns (query heads of a key head)
+  int twice_rows;             // sequences of fewer valid rows than this make each pass twice
   int step;                   // the cache's step mask (0: none); needs row_mult 1
   int chunk_log2;             // columns per chunk
   int item_cost, min_share;   // units
@@ -91,6 +92,7 @@ __device__ __forceinline__ int ceil_small(long long a, long long b) {
 struct SeqCost {
   int tiles;
   long long base, slope;
+  int twice;   // 1: each pass is made twice; a piece then takes two chunks at least
   __device__ __forceinline__ long long before(long long t) const {
     return base * t + (slope == 0 ? 0 : slope * (t * (t - 1) / 2));
   }
@@ -102,17 +104,19 @@ struct SeqCost {
 __device__ __forceinline__ int sched_round_up(const SchedParams& p, int cols) {
   return (int)(((unsigned)cols + (1u << p.chunk_log2) - 1u) >> p.chunk_log2);
 }
-__device__ __forceinline__ long long sched_chunks_of(const SchedParams& p, int cols) {
-  return (long long)sched_round_up(p, cols) * p.mult;
+__device__ __forceinline__ long long sched_chunks_of(const SchedParams& p, int cols,
+                                                     int valid_rows) {
+  return (long long)sched_round_up(p, cols) * p.mult << (valid_rows < p.twice_rows ? 1 : 0);
 }
 __device__ __forceinline__ SeqCost sched_cost(const SchedParams& p, const SeqRange& r,
                                               const SeqRange& c) {
-  SeqCost s{ceil_small((long long)r.rows * p.row_mult, p.tile_rows), 0, 0};
+  SeqCost s{ceil_small((long long)r.rows * p.row_mult, p.tile_rows), 0, 0,
+            r.valid < p.twice_rows ? 1 : 0};
   if (p.step > 0 && p.step < r.rows) {
     s.base = (long long)p.item_cost + max(c.valid - r.rows, 0) + p.tile_rows;
     s.slope = p.tile_rows;
   } else {
-    s.base = p.item_cost + (sched_chunks_of(p, c.valid) << p.chunk_log2);
+    s.base = p.item_cost + (sched_chunks_of(p, c.valid, r.valid) << p.chunk_log2);
   }
   return s;
 }
@@ -167,7 +171,7 @@ __device__ __forceinline__ SchedPlan sched_begin(const SchedParams& p, int worke
     return SchedPlan{kRounds, 0, p.items, p.ns};
   }
   const bool few = p.seqs <= 32;   // a sequence per lane: its cost stays in registers
-  SeqCost cost{0, 0, 0};
+  SeqCost cost{0, 0, 0, 0};
   long long units = 0;
   int items = 0;
   for (int b = lane; b < p.seqs; b += 32) {
@@ -183,14 +187,16 @@ __device__ __forceinline__ SchedPlan sched_begin(const SchedParams& p, int worke
   if (items == 0) return plan;
   const int one = __ffs((int)__ballot_sync(0xffffffffu, !none)) - 1;
   const long long base1 = __shfl_sync(0xffffffffu, cost.base, one);
-  if (few && __all_sync(0xffffffffu, none || (cost.base == base1 && cost.slope == 0)) &&
+  const int twice1 = p.twice_rows == 0 ? 0 : __shfl_sync(0xffffffffu, cost.twice, one);
+  if (few && __all_sync(0xffffffffu, none || (cost.base == base1 && cost.slope == 0 &&
+                                              cost.twice == twice1)) &&
       items < (1 << 20)) {
     // Equal items.  Each lane tries a number of pieces: 1 .. 30, and those that
     // fill one or two rounds.  More than two rounds only of whole items (a worker
     // has two partial slots).
     const int chunks = (int)min((base1 - p.item_cost) >> p.chunk_log2, 1ll << 20);
     int ns = lane < 30 ? lane + 1 : div_small((long long)(lane - 29) * p.grid, items);
-    ns = max(1, min(ns, chunks));
+    ns = max(1, min(ns, chunks >> twice1));
     const int rounds = ceil_small((long long)items * ns, p.grid);
     // Rounds times an item's fixed work and its chunks, both in chunks.
     long long t = (long long)rounds * (((p.item_cost - 1) >> p.chunk_log2) + 1 + ceil_small(chunks, ns));
@@ -257,7 +263,9 @@ inline void sched_plan_on_host(SchedParams* p) {
   p->items = p->ns = 0;
   if (p->row_off || p->col_off || p->col_lens || p->lengths || p->step || p->seqs != 1) return;
   const long long chunk = 1ll << p->chunk_log2;
-  const long long chunks = (p->cols + chunk - 1) / chunk * p->mult;
+  if (p->row_lens && p->twice_rows > 0) return;
+  const int twice = p->rows < p->twice_rows ? 1 : 0;
+  const long long chunks = (p->cols + chunk - 1) / chunk * p->mult << twice;
   const long long items =
       ((long long)p->rows * p->row_mult + p->tile_rows - 1) / p->tile_rows * p->heads;
   if (items == 0 || items >= (1 << 20)) return;
@@ -267,7 +275,7 @@ inline void sched_plan_on_host(SchedParams* p) {
   int best_ns = 1;
   for (int i = 0; i < 32; ++i) {
     long long ns = i < 30 ? i + 1 : (i - 29) * (long long)p->grid / items;
-    ns = ns > chunks ? chunks : ns;
+    ns = ns > chunks >> twice ? chunks >> twice : ns;
     ns = ns < 1 ? 1 : ns;
     const long long rounds = (items * ns + p->grid - 1) / p->grid;
     if (ns > 1 && rounds > 2) continue;
@@ -323,7 +331,7 @@ struct Segment {
 
 __device__ __forceinline__ long long sched_chunks(const SchedParams& p, const SeqRange& r,
                                                   const SeqRange& c, int tile) {
-  if (p.step == 0) return sched_chunks_of(p, c.valid);
+  if (p.step == 0) return sched_chunks_of(p, c.valid, r.valid);
   const int last = min((tile + 1) * p.tile_rows, r.rows) - 1;
   return sched_round_up(p, step_end(c.valid, r.rows, last, p.step));
 }

@@ -526,8 +526,9 @@ ress_status ress_cross_attn(const ress_cross_shape* shape, const void* q, const 
  *   workspace  ress_cross_bwd_workspace_bytes(shape) bytes, 256-byte aligned.
  *   P = exp(S - lse) takes lse as float32, so it is off by 2^-24 |lse|: gradients
  *   mean something for logits up to about 2^16.
- *   P enters its product as bf16, dS as bf16 for dk and as two bf16 numbers
- *   (16 bits) for dq; all sums are float32 in a fixed order.
+ *   dS enters dq as two bf16 numbers (16 bits); P enters dv, and dS dk, as one for
+ *   sequences of more than 128 keys and as two for shorter ones.  All sums are
+ *   float32 in a fixed order.
  */
 ress_status ress_cross_attn_bwd(const ress_cross_shape* shape, const void* q, const void* k,
                                 const void* v, const void* out, const float* lse,
