@@ -893,13 +893,15 @@ def ress_cache_plan(added: torch.Tensor, lengths: torch.Tensor, table: torch.Ten
     (r, width), page, tokens = table.shape, operator.index(page), operator.index(tokens)
     limit = (2 ** 31 - 1) // max(page, 1) if pages is None else operator.index(pages)
     _int32(page=page, pages=limit, tokens=tokens, free_pages=free_pages.shape[0])
+    if tokens < 0:
+        raise ValueError(f"tokens must not be negative, got {tokens}")
     ins = (_expect(added, (r,), i32, device, "added"),
            _expect(lengths, (r,), i32, device, "lengths"),
            _expect(table, (r, width), i32, device, "table"),
            _expect(free_pages, free_pages.shape, i32, device, "free_pages"),
            free_pages.shape[0], _expect(cursor, (1,), i32, device, "cursor"))
     sizes = (r + 1, tokens, r, 1)
-    if tokens >= 0 and offsets is slots is new_lengths is new_cursor is None:
+    if offsets is slots is new_lengths is new_cursor is None:
         made = _new((sum(sizes),), i32, added, stream).split_with_sizes(sizes)
         ptrs = [t.data_ptr() for t in made]
     else:

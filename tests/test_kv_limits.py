@@ -77,3 +77,11 @@ def test_binding_refuses_numbers_that_are_no_integers(ress):
         ress.ress_cache_attn(q, cache, table, one, two, step=1.5)
     with pytest.raises(TypeError):
         ress.ress_cache_plan(one, one, table, two, one, 64.5, 5)
+
+
+def test_binding_refuses_a_negative_slot_map(ress):
+    table, one, two = _on_device(torch.zeros(1, 3, dtype=torch.int32),
+                                 torch.zeros(1, dtype=torch.int32),
+                                 torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="tokens must not be negative"):
+        ress.ress_cache_plan(one, one, table, two, one, 64, -5)
