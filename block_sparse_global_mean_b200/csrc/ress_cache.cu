@@ -389,7 +389,10 @@ cudaError_t launch_append_typed(const AppendParams& p, cudaStream_t st) {
   // Runs that start in one window are written one after another.  Whole views
   // start one run per page of tokens, so a window is a page; short calls (a few
   // tokens each for many requests) start one per token or few (64 requests of one
-  // token: 3.7 us; in one window their 64 runs would follow one another).
+  // token: 3.7 us; in one window their 64 runs would follow one another).  Windows of
+  // 1, 8 and a page (64) tokens, 16 heads: 64 runs of 128 tokens 137, 20 and 12 us; 300
+  // of 20 tokens 101, 20 and 15 us; 512 of 8 tokens 70 and 20 us (1, 8); 8,192 requests
+  // of one token 264, 212 and 228 us, so a total above 4,096 of single tokens loses 7 %.
   const int window = p.tokens <= 1024 ? 1 : p.tokens <= 4096 ? 8 : p.page;
   const unsigned blocks = (unsigned)(((long long)p.tokens + window - 1) / window * p.kv_heads * 2);
   return p.page == 64

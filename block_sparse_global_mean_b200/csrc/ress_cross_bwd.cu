@@ -8,8 +8,9 @@
 // two walks are made, each with the accumulators of its own rows in TMEM: the
 // key walk (kDQ = false: tiles of 128 keys against chunks of 128 query rows) and
 // the query walk (kDQ = true: tiles of 128 query rows, the heads of a key head
-// together, against chunks of 128 keys).  S and dout V^T are computed in both:
-// seven products instead of five, no atomics.
+// together, against chunks of 128 keys).  S and dout V^T are computed in both, and
+// the query walk multiplies dS twice (below): eight products for the formula's five,
+// and the exponentials twice; no atomics.
 //
 // In both walks the resident tile gives the rows of the products, so P and dS
 // leave the registers as rows and go back to TMEM as the left operand of the

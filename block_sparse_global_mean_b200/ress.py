@@ -769,7 +769,9 @@ def ress_cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     sequences; ``q_lens`` / ``kv_lens`` ([sequences] int32) mark the rows of
     each that are not padding.  Token rows of q, k and v may be slices of
     wider rows.  Rows of no sequence are left as they were (undefined in a
-    tensor that this call allocates).  See include/ress.h."""
+    tensor that this call allocates).  Nothing is recorded for autograd, whatever
+    the inputs ask for: ress_cross_attn_bwd gives the gradients.  See
+    include/ress.h."""
     if _call is not None and out is lse is workspace is stream is None:
         done = _call.cross_attn(q, k, v, q_offsets, kv_offsets, q_lens, kv_lens, bool(want_lse))
         if done is not None:

@@ -618,7 +618,9 @@ ress_status ress_cache_plan(const ress_cache_shape* shape, const int32_t* added,
  *   (2.98e38) in magnitude: one that is not is flagged (RESS_ERR_INVALID_ARG,
  *   detail 105).  Its code is the largest number, or NaN for NaN; infinities and
  *   NaN do not count for the scale.
- *   shape->requests and max_pages are not used.  One launch, no workspace.
+ *   The scale of a page that is continued must be one that an append wrote.
+ *   tokens may be up to 2^29.  shape->requests and max_pages are not used.  One
+ *   launch, no workspace.
  */
 ress_status ress_cache_append(const ress_cache_shape* shape, const void* k, const void* v,
                               int32_t dtype, int64_t k_stride, int64_t v_stride,
@@ -644,8 +646,8 @@ size_t ress_cache_attn_workspace_bytes(const ress_cache_shape* shape, int32_t he
  *   step >= 1   end = min(lengths[r], (position / step + 1) * step): a token
  *               sees its own group of `step` tokens and the earlier ones
  *               (step 1: causal; step = tokens of a view: views in order).
- * A row that sees nothing (an empty request, a position before 0) writes 0
- * and lse -inf.  Rows of no request are left as they were.
+ * A row that sees nothing (an empty request; with a step, a position before 0)
+ * writes 0 and lse -inf.  Rows of no request are left as they were.
  *
  *   table     [requests][max_pages] int32, lengths [requests] int32, offsets
  *             [requests + 1] int32.  Flagged as RESS_ERR_BAD_INDEX: offsets
@@ -660,7 +662,12 @@ size_t ress_cache_attn_workspace_bytes(const ress_cache_shape* shape, int32_t he
  *   bf16 or f16, their sums and lse are float32.  Cells behind lengths[r] are
  *   never used as numbers.  A token before them whose key or value holds a NaN
  *   code (the append that made it was flagged) makes NaN every row that sees it,
- *   all 64 values and lse, and changes no other row.  Logits up to 2^30, as in ress_cross_attn.
+ *   all 64 values and lse, and changes no other row.  Logits up to 2^30, as in
+ *   ress_cross_attn.
+ *   tokens may be up to 2^30.  Which of two kernels serves the call is chosen from
+ *   the average query rows per request: requests that add whole views and requests
+ *   that add a token each are faster in two calls (by about half).  The kernel for
+ *   few rows reads all of a request's keys whatever the step.
  */
 ress_status ress_cache_attn(const ress_cache_shape* shape, int32_t heads, int32_t tokens,
                             const void* q, int64_t q_stride, const void* k_cache,
@@ -672,8 +679,9 @@ ress_status ress_cache_attn(const ress_cache_shape* shape, int32_t heads, int32_
 /*
  * Synchronises `stream`, then reports and clears the device error flag that
  * the kernels set: RESS_ERR_TIMEOUT (a device wait ran out of time),
- * RESS_ERR_BAD_INDEX (an idx entry outside [0, nb) was skipped), RESS_OK if
- * none, RESS_ERR_CUDA if the synchronisation itself failed.  `detail`, if not
+ * RESS_ERR_BAD_INDEX (an idx entry outside [0, nb) was skipped, or what the entry
+ * points above say), RESS_ERR_INVALID_ARG (a value or a scale that the cache does
+ * not take), RESS_OK if none, RESS_ERR_CUDA if the synchronisation itself failed.  `detail`, if not
  * NULL, receives a kernel-specific code of the first error (0 if none).
  */
 ress_status ress_check_device_errors(void* stream, int32_t* detail);
