@@ -57,7 +57,7 @@ def needs_build() -> bool:
 def call_tag() -> str:
     """The torch and Python whose object layouts the binding's C++ part holds."""
     import torch
-    return (f"torch {torch.__version__} {torch.version.git_version} "
+    return (f"torch {torch.__version__} {getattr(torch.version, 'git_version', '')} "
             f"abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)} {sysconfig.get_config_var('SOABI')}")
 
 

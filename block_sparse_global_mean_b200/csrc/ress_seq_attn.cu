@@ -25,8 +25,8 @@
 //          bf16 number 2^-120 times its value and multiplied by 2^120 * scale,
 //          which is exact for the cache's power-of-two scales, so the tensor
 //          core sees code * scale without a rounding.  NaN codes are looked for
-//          on the way (2,748 rows over
-//          45,342 tokens and two smaller requests: 880 us without, 903 us with).
+//          on the way (2,748 rows over 45,342 tokens and two smaller requests:
+//          880 us without, 903 us with).
 //
 // Keys outside a row's range get -inf before the maximum; values of such keys
 // are zeroed in shared memory (0 * NaN would reach the sums).
